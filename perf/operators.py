@@ -293,7 +293,7 @@ def _own(s):
         return [la.llama_attn_decode_paged_e4m3(s["q"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"], s["lens"],
                                                 **into)]
     ids = la.llama_attn_select_blocks(s["q"], s["bounds"], s["table"], s["lens"], s["page"], s["n_sel"], n_first=1,
-                                      n_last=1, block_ids=s["ids"], workspace=s["workspace"], rope_theta=THETA)
+                                      n_last=1, block_ids=s["ids"], rope_theta=THETA)
     if e4m3:
         return [ids, la.llama_attn_decode_paged_sparse_e4m3(s["q"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"],
                                                             ids, s["lens"], **into)]
