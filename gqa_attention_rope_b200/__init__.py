@@ -38,12 +38,20 @@ EXPORTED = (
     "llama_attn_prefill_workspace_size",
     "llama_attn_prefill_ws",
     "llama_attn_prefill_cp_ws",
+    "llama_attn_kv_append_paged",
+    "llama_attn_kv_append_paged_e4m3",
+    "llama_attn_decode_runs_workspace_size",
+    "llama_attn_decode_paged_e4m3",
+    "llama_attn_select_blocks",
+    "llama_attn_decode_paged_sparse",
+    "llama_attn_decode_paged_sparse_e4m3",
 )
 
 DEVERR_TIMEOUT = 0x1
 DEVERR_DOC_OFFSETS = 0x2
 DEVERR_CACHE_LEN = 0x4
 DEVERR_BLOCK_TABLE = 0x8
+DEVERR_BLOCK_IDS = 0x10
 
 _lock = threading.Lock()
 _lib = None
@@ -105,6 +113,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.llama_attn_prefill_ws.restype = I
     lib.llama_attn_prefill_cp_ws.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, I, P, Z, P]
     lib.llama_attn_prefill_cp_ws.restype = I
+    L = ctypes.c_int64
+    lib.llama_attn_kv_append_paged.argtypes = [P, P, L, L] + [P] * 7 + [I] * 7 + [P, I, P]
+    lib.llama_attn_kv_append_paged.restype = I
+    lib.llama_attn_kv_append_paged_e4m3.argtypes = [P, P, L, L] + [P] * 9 + [I] * 7 + [P, I, P]
+    lib.llama_attn_kv_append_paged_e4m3.restype = I
+    lib.llama_attn_decode_runs_workspace_size.argtypes = [I, I, I, I]
+    lib.llama_attn_decode_runs_workspace_size.restype = Z
+    lib.llama_attn_decode_paged_e4m3.argtypes = [P] * 9 + [I] * 8 + [F, P, Z, P]
+    lib.llama_attn_decode_paged_e4m3.restype = I
+    lib.llama_attn_select_blocks.argtypes = [P] * 5 + [I] * 11 + [F, P]
+    lib.llama_attn_select_blocks.restype = I
+    lib.llama_attn_decode_paged_sparse.argtypes = [P] * 8 + [I] * 9 + [F, P, Z, P]
+    lib.llama_attn_decode_paged_sparse.restype = I
+    lib.llama_attn_decode_paged_sparse_e4m3.argtypes = [P] * 10 + [I] * 9 + [F, P, Z, P]
+    lib.llama_attn_decode_paged_sparse_e4m3.restype = I
     return lib
 
 
@@ -490,6 +513,198 @@ def llama_attn_decode_noalloc(q, kcache, vcache, cache_lens, out, rope_theta: fl
                                          Hkv, D, Lmax, float(rope_theta), _stream(stream))
     _check("llama_attn_decode_noalloc", st)
     return out
+
+
+# ---- paged cache: append, E4M3 decode, block-sparse decode
+def _tensor(name, t, dtypes, shape, dev, contiguous=True):
+    """``t`` is a CUDA tensor on ``dev`` of one of ``dtypes`` and of ``shape`` (None: any extent)."""
+    if (t.device != dev or t.dtype not in dtypes or (contiguous and not t.is_contiguous())
+            or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name}: {'contiguous ' if contiguous else ''}{'/'.join(str(d) for d in dtypes)} tensor of "
+                         f"shape {tuple('*' if n is None else n for n in shape)} on {dev} expected, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _call(fn, dev, stream, *args):
+    """Calls the library on ``dev`` (tensors may live on another device than the
+    current one) and that device's current stream, or on ``stream``."""
+    import torch
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    _require(s.device == dev, f"stream is on {s.device}, the tensors are on {dev}")
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, s.cuda_stream)
+    if st:
+        _check(fn, st)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cuda_device(t, name):
+    _require(t.is_cuda, f"{name}: CUDA tensor expected")
+    return t.device
+
+
+def _append(fn, k, v, pools, scales, block_table, cache_lens, rope_table, new_lens, kbounds, out_lens, dtypes, stream):
+    import torch
+    i32 = (torch.int32,)
+    dev = _cuda_device(k, "k")
+    _require(k.dim() == 4, "k must be [B, T, Hkv, 128]")
+    B, T, Hkv, D = k.shape
+    strides = []
+    for name, t in (("k", k), ("v", v)):
+        _tensor(name, t, (torch.bfloat16,), (B, T, Hkv, D), dev, contiguous=False)
+        sb, st, sh, sd = t.stride()
+        _require((sd == 1 or D == 1) and (sh == D or Hkv == 1), f"{name}: the heads of a token must be contiguous")
+        strides.append((st if T > 1 else Hkv * D, sb if B > 1 else 0))
+    _require(strides[0] == strides[1], "k and v must have the same strides")
+    kpages, vpages = pools
+    _tensor("kpages", kpages, dtypes, (None, Hkv, None, D), dev)
+    n_pages, page_size = kpages.shape[0], kpages.shape[2]
+    _tensor("vpages", vpages, (kpages.dtype,), (n_pages, Hkv, page_size, D), dev)
+    for name, t in zip(("k_scales", "v_scales"), scales):
+        _tensor(name, t, (torch.float32,), (n_pages, Hkv), dev)
+    _tensor("block_table", block_table, i32, (B, None), dev)
+    _tensor("cache_lens", cache_lens, i32, (B,), dev)
+    _tensor("rope_table", rope_table, (torch.float32,), (None, D // 2, 2), dev)
+    if new_lens is not None:
+        _tensor("new_lens", new_lens, i32, (B,), dev)
+    if out_lens is not None:
+        _tensor("out_lens", out_lens, i32, (B,), dev)
+    if kbounds is not None:
+        _tensor("kbounds", kbounds, (torch.bfloat16,), (n_pages, Hkv, 2, D), dev)
+    _call(fn, dev, stream, k.data_ptr(), v.data_ptr(), *strides[0], kpages.data_ptr(), vpages.data_ptr(),
+          *(t.data_ptr() for t in scales), _addr(kbounds), block_table.data_ptr(), cache_lens.data_ptr(),
+          _addr(new_lens), _addr(out_lens), B, T, Hkv, D, page_size, block_table.shape[1], n_pages,
+          rope_table.data_ptr(), rope_table.shape[0])
+    return out_lens
+
+
+def llama_attn_kv_append_paged(k, v, kpages, vpages, block_table, cache_lens, rope_table, new_lens=None, kbounds=None,
+                               out_lens=None, stream=None):
+    """Appends k and v [B,T,Hkv,128] (bf16, un-rotated; slices of a fused
+    projection will do) behind cache_lens[b] rows of each sequence in a bf16
+    page pool [n_pages,Hkv,page_size,128], the keys rotated at their positions
+    with ``rope_table`` (llama_attn_rope_table_build, max_blocks * page_size
+    rows). new_lens int32 [B]: rows per sequence where they are fewer than T.
+    kbounds bf16 [n_pages,Hkv,2,128]: per block least and greatest key, kept for
+    llama_attn_select_blocks. out_lens int32 [B] gets the new lengths. Returns out_lens."""
+    import torch
+    return _append("llama_attn_kv_append_paged", k, v, (kpages, vpages), (), block_table, cache_lens, rope_table,
+                   new_lens, kbounds, out_lens, (torch.bfloat16,), stream)
+
+
+def llama_attn_kv_append_paged_e4m3(k, v, kpages, vpages, k_scales, v_scales, block_table, cache_lens, rope_table,
+                                    new_lens=None, kbounds=None, out_lens=None, stream=None):
+    """llama_attn_kv_append_paged into E4M3 pages (uint8 or float8_e4m3fn) with
+    one float32 scale per page and KV head, k_scales and v_scales [n_pages,Hkv]."""
+    import torch
+    return _append("llama_attn_kv_append_paged_e4m3", k, v, (kpages, vpages), (k_scales, v_scales), block_table,
+                   cache_lens, rope_table, new_lens, kbounds, out_lens, (torch.uint8, torch.float8_e4m3fn), stream)
+
+
+def llama_attn_decode_runs_workspace_size(B: int, Hq: int, Hkv: int, D: int = 128) -> int:
+    """Bytes of workspace of llama_attn_decode_paged_e4m3, _paged_sparse and _paged_sparse_e4m3."""
+    return int(lib().llama_attn_decode_runs_workspace_size(int(B), int(Hq), int(Hkv), int(D)))
+
+
+def _decode_runs(fn, q, pools, scales, block_table, block_ids, cache_lens, out, lse, workspace, q_pos_offset,
+                 rope_theta, dtypes, stream):
+    import torch
+    i32 = (torch.int32,)
+    dev = _cuda_device(q, "q")
+    _tensor("q", q, (torch.bfloat16,), (None, None, None), dev)
+    B, Hq, D = q.shape
+    kpages, vpages = pools
+    _tensor("kpages", kpages, dtypes, (None, None, None, D), dev)
+    n_pages, Hkv, page_size, _ = kpages.shape
+    _tensor("vpages", vpages, (kpages.dtype,), (n_pages, Hkv, page_size, D), dev)
+    for name, t in zip(("k_scales", "v_scales"), scales):
+        _tensor(name, t, (torch.float32,), (n_pages, Hkv), dev)
+    _tensor("block_table", block_table, i32, (B, None), dev)
+    _tensor("cache_lens", cache_lens, i32, (B,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    _tensor("out", out, (torch.bfloat16,), (B, Hq, D), dev)
+    if lse is not None:
+        _tensor("lse", lse, (torch.float32,), (B, Hq), dev)
+    if workspace is None:
+        workspace = torch.empty(max(1, llama_attn_decode_runs_workspace_size(B, Hq, Hkv, D)), dtype=torch.uint8,
+                                device=dev)
+    _require(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous tensor on {dev} expected")
+    ids, n_sel = (), ()
+    if block_ids is not None:
+        _tensor("block_ids", block_ids, i32, (B, Hkv, None), dev)
+        ids, n_sel = (block_ids.data_ptr(),), (block_ids.shape[2],)
+    _call(fn, dev, stream, q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), *(t.data_ptr() for t in scales),
+          block_table.data_ptr(), *ids, cache_lens.data_ptr(), out.data_ptr(), _addr(lse), B, Hq, Hkv, D, page_size,
+          block_table.shape[1], n_pages, *n_sel, q_pos_offset, rope_theta, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return out
+
+
+def llama_attn_decode_paged_e4m3(q, kpages, vpages, k_scales, v_scales, block_table, cache_lens, out=None, lse=None,
+                                 workspace=None, q_pos_offset: int = 0, rope_theta: float = 500000.0, stream=None):
+    """Decode of q [B,Hq,128] against an E4M3 page pool [n_pages,Hkv,page_size,128]
+    with scales [n_pages,Hkv] (llama_attn_kv_append_paged_e4m3). The query is
+    rotated at cache_lens[b] + q_pos_offset: 0 as in llama_attn_decode, -1 where
+    its own key has been appended. lse float32 [B,Hq] (optional) gets the
+    log-sum-exp. Returns out [B,Hq,128]."""
+    import torch
+    return _decode_runs("llama_attn_decode_paged_e4m3", q, (kpages, vpages), (k_scales, v_scales), block_table, None,
+                        cache_lens, out, lse, workspace, q_pos_offset, rope_theta,
+                        (torch.uint8, torch.float8_e4m3fn), stream)
+
+
+def llama_attn_select_blocks(q, kbounds, block_table, cache_lens, page_size: int, n_sel: int, n_first: int = 1,
+                             n_last: int = 1, block_ids=None, q_pos_offset: int = 0,
+                             rope_theta: float = 500000.0, stream=None):
+    """Chooses n_sel blocks per sequence and KV head for llama_attn_decode_paged_sparse:
+    the first n_first, the last n_last, and those with the greatest bound of
+    the group's products with a key of the block (kbounds, as the append keeps
+    them). Returns block_ids int32 [B,Hkv,n_sel], ascending, -1 behind the last."""
+    import torch
+    i32 = (torch.int32,)
+    dev = _cuda_device(q, "q")
+    _tensor("q", q, (torch.bfloat16,), (None, None, None), dev)
+    B, Hq, D = q.shape
+    _tensor("kbounds", kbounds, (torch.bfloat16,), (None, None, 2, D), dev)
+    n_pages, Hkv = kbounds.shape[:2]
+    _tensor("block_table", block_table, i32, (B, None), dev)
+    _tensor("cache_lens", cache_lens, i32, (B,), dev)
+    if block_ids is None:
+        block_ids = torch.empty(B, Hkv, n_sel, dtype=torch.int32, device=dev)
+    _tensor("block_ids", block_ids, i32, (B, Hkv, n_sel), dev)
+    _call("llama_attn_select_blocks", dev, stream, q.data_ptr(), kbounds.data_ptr(), block_table.data_ptr(),
+          cache_lens.data_ptr(), block_ids.data_ptr(), B, Hq, Hkv, D, page_size, block_table.shape[1], n_pages, n_sel,
+          n_first, n_last, q_pos_offset, rope_theta)
+    return block_ids
+
+
+def llama_attn_decode_paged_sparse(q, kpages, vpages, block_table, block_ids, cache_lens, out=None, lse=None,
+                                   workspace=None, q_pos_offset: int = 0, rope_theta: float = 500000.0, stream=None):
+    """Decode of q [B,Hq,128] over the blocks block_ids int32 [B,Hkv,n_sel] of a
+    bf16 page pool (ascending, each once, -1 behind the last; as
+    llama_attn_select_blocks gives them). Other arguments as for
+    llama_attn_decode_paged_e4m3. Returns out [B,Hq,128]."""
+    import torch
+    return _decode_runs("llama_attn_decode_paged_sparse", q, (kpages, vpages), (), block_table, block_ids, cache_lens,
+                        out, lse, workspace, q_pos_offset, rope_theta, (torch.bfloat16,), stream)
+
+
+def llama_attn_decode_paged_sparse_e4m3(q, kpages, vpages, k_scales, v_scales, block_table, block_ids, cache_lens,
+                                        out=None, lse=None, workspace=None, q_pos_offset: int = 0,
+                                        rope_theta: float = 500000.0, stream=None):
+    """llama_attn_decode_paged_sparse over an E4M3 page pool with its scales."""
+    import torch
+    return _decode_runs("llama_attn_decode_paged_sparse_e4m3", q, (kpages, vpages), (k_scales, v_scales), block_table,
+                        block_ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta,
+                        (torch.uint8, torch.float8_e4m3fn), stream)
 
 
 def shard_units(n_units: int, world_size: int, rank: int):

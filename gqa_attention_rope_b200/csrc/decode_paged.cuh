@@ -1,0 +1,739 @@
+// decode_paged.cuh -- single-token GQA decode over a paged cache of E4M3 codes
+// with a scale per (page, KV head), and over chosen blocks of a paged cache
+// (E4M3 or bf16): the work of the whole batch is cut into equal runs, one per
+// resident CTA.
+//
+// Mathematics, for the query heads h of a KV group and the cache rows n that
+// the call names (all rows below len, or those of the chosen blocks):
+//   s_hn = (q_h . k_n) ks_n / sqrt(128) in log2 units,  o_h = sum_n 2^(s_hn - M) vs_n v_n / sum_n 2^(s_hn - M)
+// with k_n, v_n the codes and ks_n, vs_n the scales of row n's block (1 for
+// bf16). A row's value scale is put into its exponent: P_hn = 2^(s_hn + log2
+// vs_n - m) with m a running bound of the whole exponent, so P stays within
+// range of 16 bits whatever the scales are; the denominator adds P_hn / vs_n.
+//
+// What bounds it: HBM. A row of an E4M3 cache is 256 bytes for 4 * 128 * G
+// flop. The products run on mma.sync m16n8k16 with the 16 cache rows of a warp
+// as M and the heads of the group as N (8 or 16): S^T = K Q^T, O^T = V^T P^T.
+// With heads as M, groups of 8 heads would leave half of each product empty.
+// E4M3 codes become f16 exactly (cvt.rn.f16x2.e4m3x2), so K and V carry no
+// rounding beyond their own; Q is rounded to f16 after its row is brought to
+// [0.5, 1) by a power of two (2^-12 relative; bf16 would be 2^-9), P to f16.
+// On bf16 pages the products are bf16: Q is the sum of two bf16 terms (2^-17
+// relative), P one bf16 (2^-9, the rounding of the output's own type).
+// The 8-bit rows are loaded with the 16-bit ldmatrix: each 32-bit register
+// then holds 4 neighbouring codes of a key, or 2 codes of 2 neighbouring rows
+// of V (transposed form). The products sum over d in any order, so Q is laid
+// out to match, and V's even and odd channels go to rows i and i + 8 of a tile.
+//
+// Work split: a unit is one 64-row stage of one (sequence, KV head). All units
+// of the batch in the order (sequence, head, stage) are cut into gridDim.x
+// equal runs, so ragged lengths leave no CTA idle and the ring of stages never
+// drains between sequences. A (sequence, head) inside one run is written to
+// the output directly; one that spans several leaves partial results (at most
+// two per CTA: its first and its last), which decode_join_kernel merges in
+// the order of the runs: the result does not depend on timing.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace la {
+namespace dpg {
+
+constexpr int ROWS = 64;                  // cache rows of a stage
+constexpr int NCW = 4;                    // compute warps: 16 rows of a stage each
+constexpr int NTHREADS = (NCW + 1) * 32;  // and the producer warp
+constexpr float kLift = 7.f;              // P of the greatest row: 2^7
+constexpr int MAX_CTAS = 512;             // runs (and twice as many partial results) the workspace holds
+
+template <bool kE4M3>
+struct Tile {
+  static constexpr uint32_t HALF = ROWS * 128;                    // 64 rows x 128 bytes
+  static constexpr uint32_t TENSOR = kE4M3 ? HALF : 2 * HALF;     // K or V of a stage
+  static constexpr uint32_t STAGE = 2 * TENSOR;
+  static constexpr int NSTAGE = kE4M3 ? 6 : 3;                    // 96 KB: two CTAs per SM
+  // One region for two uses that never overlap in time: the query rows (f16,
+  // or two bf16 terms) until every warp holds its fragments, and the merge
+  // scratch (two warps x 8 heads x 128 float) at a segment's end.
+  static constexpr uint32_t OFF_Q = NSTAGE * STAGE;
+  static constexpr uint32_t OFF_SCR = OFF_Q;
+  static constexpr uint32_t Q_ROW = 264;                          // bytes: 128 16-bit values, 8 bytes of padding
+  static constexpr uint32_t OFF_META = OFF_Q + (kE4M3 ? 8192 : 32 * Q_ROW);
+  static constexpr uint32_t OFF_BAR = OFF_META + NSTAGE * 16;
+  static constexpr uint32_t OFF_ML = OFF_BAR + 128;               // per warp and head: m, l
+  static constexpr uint32_t OFF_FREQ = OFF_ML + NCW * 16 * 8;     // theta_k in float64
+  static constexpr uint32_t OFF_CS = OFF_FREQ + 64 * 8;           // (cos, sin) row of the segment
+  static constexpr uint32_t OFF_QS = OFF_CS + 64 * 8;             // per head: factor of the query row
+  static constexpr uint32_t SMEM_ALLOC = OFF_QS + 64 + 1024;
+};
+
+struct Params {
+  int B, Hq, Hkv, G, page_size, max_blocks, n_pages;
+  const int32_t* lens;
+  const int32_t* block_table;
+  const int32_t* block_ids;   // [B, Hkv, n_sel], chosen blocks only
+  int n_sel;
+  const uint16_t* q;          // [B, Hq, 128] bf16 bits
+  int q_pos_offset;
+  const float* kscales;       // [n_pages, Hkv], E4M3 only
+  const float* vscales;
+  float scale_log2;
+  double rope_theta;
+  uint16_t* out;              // [B, Hq, 128] bf16
+  float* lse;                 // [B, Hq] or null
+  float* part_o;              // [2 * MAX_CTAS][G][128]
+  float2* part_ml;            // [2 * MAX_CTAS][G]
+  int64_t* prefix;            // [B + 1] units before each sequence
+  unsigned int epoch;
+};
+
+// Stages of one (sequence, KV head).
+template <bool kSparse>
+__device__ __forceinline__ int64_t stages_of(const Params& p, int b) {
+  const int len = p.lens[b];
+  if (len <= 0 || len > static_cast<int64_t>(p.max_blocks) * p.page_size) return 0;
+  if constexpr (kSparse) {
+    const int nb = (len + p.page_size - 1) / p.page_size;
+    return static_cast<int64_t>(min(nb, p.n_sel)) * (p.page_size / ROWS);
+  }
+  return (len + ROWS - 1) / ROWS;
+}
+
+// Position of a unit in the order (sequence, KV head, stage).
+struct Cursor {
+  int b, g;
+  int64_t s, nst;
+};
+
+template <bool kSparse>
+__device__ __forceinline__ void advance(const Params& p, Cursor& c, int64_t by) {
+  c.s += by;
+  while (c.b < p.B && c.s >= c.nst) {
+    c.s -= c.nst;
+    if (c.nst > 0 && ++c.g < p.Hkv) continue;
+    c.g = 0;
+    if (++c.b < p.B) c.nst = stages_of<kSparse>(p, c.b);
+  }
+}
+
+// Units [lo, hi) of run i of n over `total` units.
+__device__ __forceinline__ int64_t run_start(int64_t total, int64_t n, int64_t i) { return total * i / n; }
+// The run that holds unit u.
+__device__ __forceinline__ int64_t run_of(int64_t total, int64_t n, int64_t u) { return ((u + 1) * n - 1) / total; }
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The two codes in the low (high) half of w as f16x2.
+__device__ __forceinline__ uint32_t f16x2_of_lo(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(h) : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t f16x2_of_hi(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}" : "=r"(h) : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// kWide: more than 8 query heads per KV head (two tiles of 8).
+template <bool kE4M3, bool kSparse, bool kWide>
+__global__ void __launch_bounds__(NTHREADS, 2)
+    decode_runs_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const Params p) {
+  using T = Tile<kE4M3>;
+  constexpr int NT = kWide ? 2 : 1;
+  constexpr int NQ = kE4M3 ? 1 : 2;  // terms of Q
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  auto full = [&](uint32_t s) { return sbase + T::OFF_BAR + 8u * s; };
+  auto empty = [&](uint32_t s) { return sbase + T::OFF_BAR + 8u * (T::NSTAGE + s); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtx wc{p.epoch};
+
+  __shared__ int64_t s_start_s, s_start_nst;
+  __shared__ int s_start_b, s_start_g;
+  __shared__ int64_t s_part[NTHREADS];
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::NSTAGE; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), NCW);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (threadIdx.x < 64)
+    reinterpret_cast<double*>(smem + T::OFF_FREQ)[threadIdx.x] =
+        pow(p.rope_theta, -2.0 * static_cast<double>(threadIdx.x) / 128.0);
+  // Units before this thread's share of the sequences, and in all: thread i
+  // takes sequences [i * per, (i + 1) * per).
+  const int per = (p.B + NTHREADS - 1) / NTHREADS;
+  const int my0 = min(p.B, static_cast<int>(threadIdx.x) * per), my1 = min(p.B, my0 + per);
+  {
+    int64_t sum = 0;
+    for (int b = my0; b < my1; ++b) sum += stages_of<kSparse>(p, b) * p.Hkv;
+    s_part[threadIdx.x] = sum;
+  }
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int i = 0; i < NTHREADS && i * per < p.B; ++i) {
+    if (i == static_cast<int>(threadIdx.x)) before = total;
+    total += s_part[i];
+  }
+  if (my0 < p.B && blockIdx.x == 0) {  // the joining kernel reads these
+    int64_t at = before;
+    for (int b = my0; b < my1; ++b) {
+      p.prefix[b] = at;
+      at += stages_of<kSparse>(p, b) * p.Hkv;
+    }
+    if (my1 == p.B) p.prefix[p.B] = at;
+  }
+  if (total == 0) return;
+  const int64_t n_runs = min(static_cast<int64_t>(gridDim.x), total);
+  if (blockIdx.x >= n_runs) return;
+  const int64_t u0 = run_start(total, n_runs, blockIdx.x), u1 = run_start(total, n_runs, blockIdx.x + 1);
+  if (my0 < my1 && before <= u0 && u0 < before + s_part[threadIdx.x]) {  // one thread finds the start
+    int64_t at = before;
+    for (int b = my0; b < my1; ++b) {
+      const int64_t nst = stages_of<kSparse>(p, b), n = nst * p.Hkv;
+      if (u0 < at + n) {
+        s_start_b = b;
+        s_start_g = static_cast<int>((u0 - at) / nst);
+        s_start_s = (u0 - at) % nst;
+        s_start_nst = nst;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  Cursor cur{s_start_b, s_start_g, s_start_s, s_start_nst};
+
+  if (warp == NCW) {
+    // ------------------------------------------------------------ producer
+    // The lanes resolve the next 32 units (block id, page, scales: dependent
+    // loads) while lane 0 issues the copies of the present 32.
+    const int rpp = p.page_size;
+    const int64_t pool_rows = static_cast<int64_t>(p.n_pages) * p.Hkv * rpp;
+    Cursor c = cur;
+    int64_t u = u0 + lane;
+    if (lane > 0) advance<kSparse>(p, c, lane);
+    struct Unit {
+      int row, nvalid;   // first row in the pool, rows below len (0: nothing to load)
+      float ks, vs;
+    };
+    auto resolve = [&]() {
+      Unit r{0, 0, 1.f, 1.f};
+      if (u >= u1) return r;
+      const int len = p.lens[c.b];
+      int n;  // the unit's first cache row
+      if constexpr (kSparse) {
+        const int spp = rpp / ROWS;
+        const int e = static_cast<int>(c.s) / spp;
+        const int32_t* ids = p.block_ids + (static_cast<int64_t>(c.b) * p.Hkv + c.g) * p.n_sel;
+        const int id = ids[e], prev = e > 0 ? ids[e - 1] : -2;
+        const int nb = (len + rpp - 1) / rpp;
+        // ascending, no id twice, -1 only behind the last one
+        const bool use = id >= 0 && id < nb && (e == 0 || (prev >= 0 && prev < id));
+        if (!use) {
+          if (id != -1) raise_error(LLAMA_ATTN_DEVERR_BLOCK_IDS);
+          return r;
+        }
+        n = id * rpp + (static_cast<int>(c.s) - e * spp) * ROWS;
+        if (n >= len) return r;
+      } else {
+        n = static_cast<int>(c.s) * ROWS;
+      }
+      r.nvalid = min(ROWS, len - n);
+      const int page = p.block_table[static_cast<int64_t>(c.b) * p.max_blocks + n / rpp];
+      if (page < 0 || page >= p.n_pages) {
+        raise_error(LLAMA_ATTN_DEVERR_BLOCK_TABLE);
+        r.row = static_cast<int>(pool_rows);  // past the pool: the copy reads zeros
+      } else {
+        r.row = (page * p.Hkv + c.g) * rpp + n % rpp;
+        if constexpr (kE4M3) {
+          r.ks = __ldg(p.kscales + static_cast<int64_t>(page) * p.Hkv + c.g);
+          r.vs = __ldg(p.vscales + static_cast<int64_t>(page) * p.Hkv + c.g);
+        }
+      }
+      return r;
+    };
+    const int n_units = static_cast<int>(u1 - u0);
+    Unit next = resolve();
+    bool alive = true;
+    int done = 0;
+    for (int i0 = 0; i0 < n_units && alive; i0 += 32) {
+      const Unit now = next;
+      u += 32;
+      if (u < u1) advance<kSparse>(p, c, 32);
+      next = resolve();
+      // a scale outside [2^-100, 2^119] would leave the range of the exponent trick
+      const float vs = fminf(fmaxf(now.vs, 7.888609e-31f), 6.646140e35f);
+      const float lv = kE4M3 ? __log2f(vs) : 0.f, iv = kE4M3 ? 1.f / vs : 1.f;
+      const int m = min(32, n_units - i0);
+      for (int j = 0; j < m; ++j) {
+        const int row = __shfl_sync(0xffffffffu, now.row, j);
+        const int nvalid = __shfl_sync(0xffffffffu, now.nvalid, j);
+        const float ks = __shfl_sync(0xffffffffu, now.ks, j);
+        const float l2 = __shfl_sync(0xffffffffu, lv, j), inv = __shfl_sync(0xffffffffu, iv, j);
+        const uint32_t st = static_cast<uint32_t>(i0 + j) % T::NSTAGE;
+        const int use = (i0 + j) / T::NSTAGE;
+        int ok = 1;
+        if (lane == 0) {
+          ok = use == 0 || mbar_wait(empty(st), (use - 1) & 1, wc);
+          if (ok) {
+            const uint32_t dst = sbase + st * T::STAGE;
+            if (nvalid > 0) {
+              if constexpr (kE4M3) {
+                tma_load_2d(dst, &tm_k, full(st), 0, row);
+                tma_load_2d(dst + T::TENSOR, &tm_v, full(st), 0, row);
+              } else {
+                tma_load_2d(dst, &tm_k, full(st), 0, row);
+                tma_load_2d(dst + T::HALF, &tm_k, full(st), 64, row);
+                tma_load_2d(dst + T::TENSOR, &tm_v, full(st), 0, row);
+                tma_load_2d(dst + T::TENSOR + T::HALF, &tm_v, full(st), 64, row);
+              }
+            }
+            *reinterpret_cast<float4*>(smem + T::OFF_META + st * 16) =
+                make_float4(__int_as_float(nvalid), ks, l2, inv);
+            if (nvalid > 0)
+              mbar_arrive_expect_tx(full(st), T::STAGE);
+            else
+              mbar_arrive(full(st));
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+          alive = false;
+          break;
+        }
+        ++done;
+      }
+    }
+    if (lane == 0)  // copies in flight land before the CTA's shared memory goes
+      for (int st = 0; st < T::NSTAGE; ++st)
+        if (done > st) mbar_wait(full(st), ((done - 1 - st) / T::NSTAGE) & 1, wc);
+    return;
+  }
+
+  // -------------------------------------------------------------- compute warps
+  const int gq = lane >> 2, t = lane & 3;
+  const int G = p.G;
+  auto bar = [] { asm volatile("bar.sync 1, %0;" ::"r"(NCW * 32) : "memory"); };
+  uint32_t qb[NQ][NT][8][2];
+  float qf[NT][2];
+  float m[NT][2], l[NT][2];
+  float o[NT][8][4];
+
+  // The rotated query rows of (b, g) as B fragments of the score product.
+  auto load_query = [&]() {
+    float2* cs_row = reinterpret_cast<float2*>(smem + T::OFF_CS);
+    if (threadIdx.x < 64) {
+      double sn, cs;
+      sincos(static_cast<double>(p.lens[cur.b] + p.q_pos_offset) *
+                 reinterpret_cast<const double*>(smem + T::OFF_FREQ)[threadIdx.x], &sn, &cs);
+      cs_row[threadIdx.x] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
+    }
+    bar();
+    for (int h = warp; h < 8 * NT; h += NCW) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (h < G) {
+        const uint2 u = *reinterpret_cast<const uint2*>(
+            p.q + (static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h) * 128 + 4 * lane);
+        const float4 cs = reinterpret_cast<const float4*>(cs_row)[lane];
+        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
+        x[0] = a.x * cs.x - a.y * cs.y;
+        x[1] = a.x * cs.y + a.y * cs.x;
+        x[2] = b.x * cs.z - b.y * cs.w;
+        x[3] = b.x * cs.w + b.y * cs.z;
+      }
+      uint8_t* row = smem + T::OFF_Q + h * T::Q_ROW + 8 * lane;
+      if constexpr (kE4M3) {
+        float am = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, s));
+        // bring the row's greatest magnitude to [0.5, 1): exact, and undone in the scores' factor
+        const int e = am > 0.f ? min(max(static_cast<int>(__float_as_uint(am) >> 23) - 126, -100), 120) : 0;
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        *reinterpret_cast<uint2*>(row) = make_uint2(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f));
+        if (lane == 0)
+          reinterpret_cast<float*>(smem + T::OFF_QS)[h] =
+              p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      } else {
+        float r[4];
+        uint32_t hi[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+          const float2 v = unpack_bf16x2(hi[i]);
+          r[2 * i] = x[2 * i] - v.x;
+          r[2 * i + 1] = x[2 * i + 1] - v.y;
+        }
+        *reinterpret_cast<uint2*>(row) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(row + 16 * T::Q_ROW) = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+      }
+    }
+    bar();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (kE4M3)
+          qf[nt][e] = reinterpret_cast<const float*>(smem + T::OFF_QS)[8 * nt + 2 * t + e];
+        else
+          qf[nt][e] = p.scale_log2;
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+#pragma unroll
+        for (int term = 0; term < NQ; ++term) {
+          const uint8_t* row = smem + T::OFF_Q + (16 * term + 8 * nt + gq) * T::Q_ROW + 32 * c;
+          if constexpr (kE4M3) {  // codes 4t .. 4t+3 of a 16-byte chunk
+            const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * t);
+            qb[term][nt][c][0] = v.x;
+            qb[term][nt][c][1] = v.y;
+          } else {
+            qb[term][nt][c][0] = *reinterpret_cast<const uint32_t*>(row + 4 * t);
+            qb[term][nt][c][1] = *reinterpret_cast<const uint32_t*>(row + 16 + 4 * t);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][c][e] = 0.f;
+      }
+    }
+  };
+
+  // Joins the four warps' results of the segment that ends here, and writes it.
+  auto finish = [&](int64_t first_unit, int64_t last_unit) {
+    float2* ml = reinterpret_cast<float2*>(smem + T::OFF_ML);  // [warp][head]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+        if (gq == 0) ml[warp * 16 + 8 * nt + 2 * t + e] = make_float2(m[nt][e], l[nt][e]);
+      }
+    bar();
+    float M[NT][2], L[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NCW; ++w) mx = fmaxf(mx, ml[w * 16 + 8 * nt + 2 * t + e].x);
+#pragma unroll
+        for (int w = 0; w < NCW; ++w) {
+          const float2 v = ml[w * 16 + 8 * nt + 2 * t + e];
+          if (v.x > -INFINITY || v.x != v.x) sum += v.y * ex2_approx(v.x - mx);
+          else sum += v.y;  // no row: zero; a NaN stays one
+        }
+        M[nt][e] = mx;
+        L[nt][e] = sum;
+        const float f = m[nt][e] == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mx);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          o[nt][c][e] *= f;
+          o[nt][c][2 + e] *= f;
+        }
+      }
+    float* scr = reinterpret_cast<float*>(smem + T::OFF_SCR);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int half = NCW / 2; half > 0; half >>= 1) {
+        if (nt > 0 || half < NCW / 2) bar();  // the scratch of the step before has been read
+        if (warp >= half && warp < 2 * half) {
+          float4* dst = reinterpret_cast<float4*>(scr + (warp - half) * 1024);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dst[c * 32 + lane] = make_float4(o[nt][c][0], o[nt][c][1], o[nt][c][2], o[nt][c][3]);
+        }
+        bar();
+        if (warp < half) {
+          const float4* src = reinterpret_cast<const float4*>(scr + warp * 1024);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 v = src[c * 32 + lane];
+            o[nt][c][0] += v.x, o[nt][c][1] += v.y, o[nt][c][2] += v.z, o[nt][c][3] += v.w;
+          }
+        }
+      }
+    }
+    if (warp == 0) {
+      const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = 8 * nt + 2 * t + e;
+          if (h >= G) continue;
+          const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
+          const float inv = L[nt][e] == 0.f ? 0.f : 1.f / L[nt][e];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float x = o[nt][c][e], y = o[nt][c][2 + e];
+            if constexpr (kE4M3) {  // channels 16c + 2gq, + 1
+              if (whole)
+                *reinterpret_cast<uint32_t*>(p.out + head * 128 + 16 * c + 2 * gq) = pack_bf16x2(x * inv, y * inv);
+              else
+                *reinterpret_cast<float2*>(p.part_o + (slot * G + h) * 128 + 16 * c + 2 * gq) = make_float2(x, y);
+            } else {  // channels 16c + gq and 16c + 8 + gq
+              if (whole) {
+                const uint32_t w = pack_bf16x2(x * inv, y * inv);
+                p.out[head * 128 + 16 * c + gq] = static_cast<uint16_t>(w & 0xFFFFu);
+                p.out[head * 128 + 16 * c + 8 + gq] = static_cast<uint16_t>(w >> 16);
+              } else {
+                p.part_o[(slot * G + h) * 128 + 16 * c + gq] = x;
+                p.part_o[(slot * G + h) * 128 + 16 * c + 8 + gq] = y;
+              }
+            }
+          }
+          if (gq == 0) {
+            if (!whole)
+              p.part_ml[slot * G + h] = make_float2(M[nt][e], L[nt][e]);
+            else if (p.lse)
+              p.lse[head] = L[nt][e] == 0.f ? -INFINITY : (M[nt][e] + log2f(L[nt][e])) * 0.6931471805599453f;
+          }
+        }
+    }
+    bar();  // scratch and (m, l) may be written again
+  };
+
+  load_query();
+  const int rbase = 16 * warp;
+  const int n_units = static_cast<int>(u1 - u0);
+  int64_t seg_first = u0 - cur.s;  // the segment's first unit (it may lie in an earlier run)
+  bool alive = true;  // false once a wait gave up: the barriers of a segment's end are still met
+  for (int i = 0; i < n_units; ++i) {
+    const uint32_t st = static_cast<uint32_t>(i) % T::NSTAGE;
+    if (alive) alive = mbar_wait(full(st), (i / T::NSTAGE) & 1, wc);
+    alive = __all_sync(0xffffffffu, alive);
+    const float4 meta = *reinterpret_cast<const float4*>(smem + T::OFF_META + st * 16);
+    const int nvalid = __float_as_int(meta.x);
+    if (alive && rbase < nvalid) {
+      const uint32_t kbase = sbase + st * T::STAGE, vbase = kbase + T::TENSOR;
+      const int mi = lane >> 3, rr = lane & 7;
+      float sc[NT][4], sd[NT][4];  // two chains of products
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = sd[nt][e] = 0.f;
+      if constexpr (kE4M3) {
+        const int row = rbase + 8 * (mi & 1) + rr;
+#pragma unroll
+        for (int c = 0; c < 8; c += 2) {
+          uint32_t w0, w1, w2, w3;  // rows 0-7 and 8-15 of chunk c, then of chunk c + 1
+          ldmatrix_x4(kbase + sw128_off(row, c + (mi >> 1)), w0, w1, w2, w3);
+          const uint32_t a[4] = {f16x2_of_lo(w0), f16x2_of_lo(w1), f16x2_of_hi(w0), f16x2_of_hi(w1)};
+          const uint32_t b[4] = {f16x2_of_lo(w2), f16x2_of_lo(w3), f16x2_of_hi(w2), f16x2_of_hi(w3)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_16816(sc[nt], a, qb[0][nt][c][0], qb[0][nt][c][1]);
+            mma_f16_16816(sd[nt], b, qb[0][nt][c + 1][0], qb[0][nt][c + 1][1]);
+          }
+        }
+      } else {
+        const int row = rbase + 8 * (mi & 1) + rr;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int d8 = 2 * c + (mi >> 1);  // 16-byte chunk of 8 channels
+          uint32_t a0, a1, a2, a3;
+          ldmatrix_x4(kbase + (d8 >> 3) * T::HALF + sw128_off(row, d8 & 7), a0, a1, a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16_16816(sc[nt], a0, a1, a2, a3, qb[0][nt][c][0], qb[0][nt][c][1]);
+            mma_bf16_16816(sd[nt], a0, a1, a2, a3, qb[NQ - 1][nt][c][0], qb[NQ - 1][nt][c][1]);
+          }
+        }
+      }
+      const bool in0 = rbase + gq < nvalid, in1 = rbase + 8 + gq < nvalid;
+      float lv = 0.f, iv = 1.f;
+      if constexpr (kE4M3) lv = meta.z, iv = meta.w;
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = kE4M3 ? qf[nt][e & 1] * meta.y : qf[nt][e & 1];
+          const float s = (sc[nt][e] + sd[nt][e]) * f + lv;
+          sc[nt][e] = ((e & 2) ? in1 : in0) ? s : -INFINITY;
+          above |= sc[nt][e] > m[nt][e & 1] + (kLift + 8.f);
+        }
+      // m is the exponents' maximum less kLift, and only has to stay within 2^8
+      // of that: it moves when some row passes it by more, seldom after the
+      // first stages. P then reaches 2^15 at most, and f16 holds P down to
+      // 2^-32 of the greatest.
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mx = fmaxf(mx - kLift, m[nt][e]);
+            const float alpha = mx == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mx);
+            m[nt][e] = mx;
+            l[nt][e] *= alpha;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              o[nt][c][e] *= alpha;
+              o[nt][c][2 + e] *= alpha;
+            }
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(sc[nt][e] - m[nt][e & 1]);
+        l[nt][0] += (pr[0] + pr[2]) * iv;
+        l[nt][1] += (pr[1] + pr[3]) * iv;
+        if constexpr (kE4M3) {
+          pb[nt][0] = movmatrix_trans(pack_f16x2(pr[0], pr[1]));
+          pb[nt][1] = movmatrix_trans(pack_f16x2(pr[2], pr[3]));
+        } else {
+          pb[nt][0] = movmatrix_trans(pack_bf16x2(pr[0], pr[1]));
+          pb[nt][1] = movmatrix_trans(pack_bf16x2(pr[2], pr[3]));
+        }
+      }
+      // value rows at or past len may hold anything (NaN included): zero them so
+      // that P = 0 cannot meet NaN inside the product.
+      const bool tail = rbase + 16 > nvalid;
+      if (tail) {
+        constexpr int kChunks = kE4M3 ? 8 : 16;  // 16-byte chunks of a row
+        for (int x = lane; x < 16 * kChunks; x += 32) {
+          const int r = rbase + x / kChunks, ch = x % kChunks;
+          if (r >= nvalid)
+            *reinterpret_cast<uint4*>(smem + st * T::STAGE + T::TENSOR + (ch >> 3) * T::HALF + r * 128 + (ch & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+      }
+      if constexpr (kE4M3) {
+        const int row = rbase + 8 * (mi & 1) + rr;
+#pragma unroll
+        for (int c = 0; c < 8; c += 2) {
+          uint32_t w[4];  // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
+          ldmatrix_x4_trans(vbase + sw128_off(row, c + (mi >> 1)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], 0u, 0x3120);  // even channels low, odd high
+          const uint32_t a[4] = {f16x2_of_lo(w[0]), f16x2_of_hi(w[0]), f16x2_of_lo(w[1]), f16x2_of_hi(w[1])};
+          const uint32_t b[4] = {f16x2_of_lo(w[2]), f16x2_of_hi(w[2]), f16x2_of_lo(w[3]), f16x2_of_hi(w[3])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_16816(o[nt][c], a, pb[nt][0], pb[nt][1]);
+            mma_f16_16816(o[nt][c + 1], b, pb[nt][0], pb[nt][1]);
+          }
+        }
+      } else {
+        const int row = rbase + 8 * (mi >> 1) + rr;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int d8 = 2 * c + (mi & 1);
+          uint32_t a0, a1, a2, a3;
+          ldmatrix_x4_trans(vbase + (d8 >> 3) * T::HALF + sw128_off(row, d8 & 7), a0, a1, a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[nt][c], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+      }
+      if (tail) fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (alive && lane == 0) mbar_arrive(empty(st));
+    if (cur.s + 1 == cur.nst || i + 1 == n_units) {
+      finish(seg_first, seg_first + cur.nst);
+      if (i + 1 < n_units) {
+        advance<kSparse>(p, cur, 1);
+        seg_first = u0 + i + 1;
+        load_query();
+      }
+    } else {
+      ++cur.s;
+    }
+  }
+}
+
+// One block per (sequence, query head), four warps: merges the partial results
+// of the runs that share it, in the order of the runs; a head written whole by
+// one run is left alone, a sequence without rows gets zeros.
+template <bool kSparse>
+__global__ void __launch_bounds__(128) decode_join_kernel(const Params p, int max_runs) {
+  const int64_t head = blockIdx.x;
+  const int b = static_cast<int>(head / p.Hq), hq = static_cast<int>(head % p.Hq);
+  const int g = hq / p.G, h = hq % p.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = p.lens[b];
+  if (hq == 0 && threadIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(p.max_blocks) * p.page_size))
+    raise_error(LLAMA_ATTN_DEVERR_CACHE_LEN);
+  const int64_t nst = stages_of<kSparse>(p, b);
+  if (nst == 0) {
+    p.out[head * 128 + threadIdx.x] = 0;
+    if (p.lse && threadIdx.x == 0) p.lse[head] = -INFINITY;
+    return;
+  }
+  const int64_t total = p.prefix[p.B], first = p.prefix[b] + g * nst;
+  const int64_t n_runs = min(static_cast<int64_t>(max_runs), total);
+  const int c0 = static_cast<int>(run_of(total, n_runs, first));
+  const int c1 = static_cast<int>(run_of(total, n_runs, first + nst - 1));
+  if (c0 == c1) return;
+  auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
+  __shared__ float s_m[4];
+  __shared__ float s_l[4];
+  __shared__ float4 s_o[4][32];
+  float M = -INFINITY;
+  for (int c = c0 + static_cast<int>(threadIdx.x); c <= c1; c += 128) M = fmaxf(M, p.part_ml[slot(c)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_m[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const int64_t at = slot(c);
+    const float2 ml = p.part_ml[at];
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+    const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - M);  // no row: zeros, or a NaN
+    L += w * ml.y;
+    acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+  }
+  s_o[warp][lane] = acc;
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  L = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const float* so = reinterpret_cast<const float*>(s_o);
+  const int d = threadIdx.x;
+  const float x = (so[d] + so[128 + d]) + (so[256 + d] + so[384 + d]);
+  const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : x / L);
+  p.out[head * 128 + d] = *reinterpret_cast<const uint16_t*>(&y);
+  if (p.lse && d == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+}  // namespace dpg
+}  // namespace la

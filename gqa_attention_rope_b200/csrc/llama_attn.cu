@@ -16,8 +16,11 @@
 #include "prefill_bf16.cuh"
 #include "qkv_fp8.cuh"
 #include "decode.cuh"
+#include "decode_paged.cuh"
+#include "paged_append.cuh"
+#include "select_blocks.cuh"
 
-#define LLAMA_ATTN_VERSION 300  // 0.3.0: caller-workspace prefill entry points, caller-owned RoPE table
+#define LLAMA_ATTN_VERSION 400  // 0.4.0: paged-cache append, E4M3 paged decode, block-sparse decode
 
 namespace {
 
@@ -257,6 +260,13 @@ int device_setup(int dev, int* n_sm) {
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<false>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<true>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::q8::qkv_fp8_rope_kernel), la::q8::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, false>), la::dpg::Tile<true>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, true>), la::dpg::Tile<true>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, false>), la::dpg::Tile<true>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, true>), la::dpg::Tile<true>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, false>), la::dpg::Tile<false>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, true>), la::dpg::Tile<false>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::sel::select_blocks_kernel), la::sel::MAX_BLOCKS * 8);
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) ds.n_sm = n;
     ds.status = st;
@@ -888,6 +898,328 @@ int llama_attn_decode_paged(const llama_attn_bf16* q, const llama_attn_bf16* kpa
   std::lock_guard<std::mutex> lock(g_mutex);
   return decode_launch(q, tk, tv, cache_lens, out, B, Hq, Hkv, Lmax, rope_theta, block_table, page_size, max_blocks,
                        n_pages, workspace, stream);
+}
+
+}  // extern "C"
+
+// ---- paged cache: append, E4M3 decode, block-sparse decode
+
+namespace {
+
+bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// The page pool's geometry and the kernels' index limits, before any launch.
+int check_pages(int B, int Hkv, int D, int page_size, int max_blocks, int n_pages) {
+  if (B <= 0 || Hkv <= 0 || page_size <= 0 || max_blocks <= 0 || n_pages <= 0) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (D != 128 || page_size % la::dpg::ROWS != 0) return LLAMA_ATTN_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535) return LLAMA_ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_blocks) * page_size >= INT32_MAX) return LLAMA_ATTN_ERR_UNSUPPORTED;
+  // page_size <= 2^31 / n_pages / Hkv: no product below overflows
+  if (static_cast<int64_t>(n_pages) * Hkv >= INT32_MAX ||
+      static_cast<int64_t>(n_pages) * Hkv * page_size >= INT32_MAX - page_size)
+    return LLAMA_ATTN_ERR_UNSUPPORTED;
+  return LLAMA_ATTN_OK;
+}
+
+struct AppendArgs {
+  const llama_attn_bf16 *k, *v;
+  int64_t row_stride, batch_stride;
+  void *kpages, *vpages;
+  float *kscales, *vscales;
+  llama_attn_bf16* kbounds;
+  const int32_t *block_table, *cache_lens, *new_lens;
+  int32_t* out_lens;
+  int B, T, Hkv, D, page_size, max_blocks, n_pages;
+  const void* rope_table;
+  int rope_rows;
+};
+
+template <bool kE4M3>
+int kv_append_paged(const AppendArgs& a, cudaStream_t stream) {
+  if (!a.k || !a.v || !a.kpages || !a.vpages || !a.block_table || !a.cache_lens || !a.rope_table)
+    return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (kE4M3 && (!a.kscales || !a.vscales)) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (a.T <= 0) return LLAMA_ATTN_ERR_INVALID_ARG;
+  int st = check_pages(a.B, a.Hkv, a.D, a.page_size, a.max_blocks, a.n_pages);
+  if (st) return st;
+  const int64_t row = static_cast<int64_t>(a.Hkv) * 128;
+  if (a.row_stride < row || a.row_stride % 8 != 0 || a.batch_stride % 8 != 0 || a.batch_stride < 0)
+    return LLAMA_ATTN_ERR_INVALID_ARG;
+  // rows of one sequence, and sequences, must not overlap into 64-bit wrap-around
+  if (a.row_stride > (int64_t(1) << 31) || a.batch_stride > (int64_t(1) << 47)) return LLAMA_ATTN_ERR_UNSUPPORTED;
+  if (a.rope_rows < static_cast<int64_t>(a.max_blocks) * a.page_size) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (!aligned16(a.k) || !aligned16(a.v) || !aligned16(a.kpages) || !aligned16(a.vpages) || !aligned16(a.rope_table) ||
+      !aligned16(a.kbounds))
+    return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (a.out_lens && ranges_overlap(a.out_lens, sizeof(int32_t) * a.B, a.cache_lens, sizeof(int32_t) * a.B))
+    return LLAMA_ATTN_ERR_INVALID_ARG;
+  la::pap::Params p;
+  p.k = a.k;
+  p.v = a.v;
+  p.row_stride = a.row_stride;
+  p.batch_stride = a.batch_stride;
+  p.kpages = a.kpages;
+  p.vpages = a.vpages;
+  p.kscales = a.kscales;
+  p.vscales = a.vscales;
+  p.kbounds = a.kbounds;
+  p.block_table = a.block_table;
+  p.lens = a.cache_lens;
+  p.new_lens = a.new_lens;
+  p.out_lens = a.out_lens;
+  p.tab = static_cast<const float4*>(a.rope_table);
+  p.T = a.T;
+  p.Hkv = a.Hkv;
+  p.page_size = a.page_size;
+  p.max_blocks = a.max_blocks;
+  p.n_pages = a.n_pages;
+  // blocks that T rows can touch, wherever in a block they begin
+  int64_t slots = (static_cast<int64_t>(a.T) + a.page_size - 2) / a.page_size + 1;
+  if (slots > a.max_blocks) slots = a.max_blocks;
+  const dim3 grid(static_cast<unsigned>(slots), a.Hkv, a.B);
+  std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
+  prof_count(1);
+  const int pair = prof_before(stream);
+  const int rows = a.T < a.page_size ? a.T : a.page_size;  // a CTA's rows at most
+  if (rows <= 16)
+    la::pap::kv_append_paged_kernel<kE4M3, 64><<<grid, 64, 0, stream>>>(p);
+  else if (rows <= 64)
+    la::pap::kv_append_paged_kernel<kE4M3, 256><<<grid, 256, 0, stream>>>(p);
+  else
+    la::pap::kv_append_paged_kernel<kE4M3, 512><<<grid, 512, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  prof_after(pair, stream);
+  return cuda_status(e);
+}
+
+// Workspace of decode_runs_kernel: units before each sequence, then (m, l)
+// and O of at most two partial results per run, each part 256-byte aligned.
+struct RunsWs {
+  size_t ml_off, o_off, total;
+};
+RunsWs runs_ws_layout(int64_t B, int64_t G) {
+  RunsWs L;
+  L.ml_off = align256(static_cast<size_t>(B + 1) * sizeof(int64_t));
+  L.o_off = L.ml_off + align256(static_cast<size_t>(2 * la::dpg::MAX_CTAS * G) * sizeof(float2));
+  L.total = L.o_off + align256(static_cast<size_t>(2 * la::dpg::MAX_CTAS * G) * 128 * sizeof(float));
+  return L;
+}
+
+struct RunsArgs {
+  const llama_attn_bf16* q;
+  const void *kpages, *vpages;
+  const float *kscales, *vscales;
+  const int32_t *block_table, *block_ids, *cache_lens;
+  llama_attn_bf16* out;
+  float* lse;
+  int B, Hq, Hkv, D, page_size, max_blocks, n_pages, n_sel, q_pos_offset;
+  float rope_theta;
+  void* workspace;
+  size_t workspace_bytes;
+};
+
+template <bool kE4M3, bool kSparse>
+int decode_runs(const RunsArgs& a, cudaStream_t stream) {
+  int st = check_decode(a.q, a.kpages, a.vpages, a.cache_lens, a.out, a.B, a.Hq, a.Hkv, a.D, a.rope_theta);
+  if (st) return st;
+  if (!a.block_table || (kSparse && !a.block_ids) || (kE4M3 && (!a.kscales || !a.vscales)))
+    return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (kSparse && a.n_sel <= 0) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (a.q_pos_offset != 0 && a.q_pos_offset != -1) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if ((st = check_pages(a.B, a.Hkv, a.D, a.page_size, a.max_blocks, a.n_pages))) return st;
+  if (static_cast<int64_t>(a.B) * a.Hkv * a.max_blocks >= (int64_t(1) << 37) / (a.page_size / la::dpg::ROWS))
+    return LLAMA_ATTN_ERR_UNSUPPORTED;  // a run's units are counted in 32 bits
+  const size_t rows_bytes = static_cast<size_t>(a.B) * a.Hq * 256;
+  if (ranges_overlap(a.out, rows_bytes, a.q, rows_bytes)) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(a.lse) & 3u) return LLAMA_ATTN_ERR_INVALID_ARG;
+  const int G = a.Hq / a.Hkv;
+  const RunsWs L = runs_ws_layout(a.B, G);
+  if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || a.workspace_bytes < L.total)
+    return LLAMA_ATTN_ERR_WORKSPACE;
+  int dev, n_sm = 148;
+  if ((st = current_device(&dev))) return st;
+  if ((st = device_setup(dev, &n_sm))) return st;
+  CUtensorMap tk, tv;
+  const int64_t rows = static_cast<int64_t>(a.n_pages) * a.Hkv * a.page_size;
+  if constexpr (kE4M3) {
+    if ((st = tmap_2d(&tk, a.kpages, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, 128, 128, la::dpg::ROWS))) return st;
+    if ((st = tmap_2d(&tv, a.vpages, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, 128, 128, la::dpg::ROWS))) return st;
+  } else {
+    if ((st = tmap_rows(&tk, a.kpages, rows))) return st;
+    if ((st = tmap_rows(&tv, a.vpages, rows))) return st;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  la::dpg::Params p;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = G;
+  p.page_size = a.page_size;
+  p.max_blocks = a.max_blocks;
+  p.n_pages = a.n_pages;
+  p.lens = a.cache_lens;
+  p.block_table = a.block_table;
+  p.block_ids = a.block_ids;
+  p.n_sel = a.n_sel;
+  p.q = a.q;
+  p.q_pos_offset = a.q_pos_offset;
+  p.kscales = a.kscales;
+  p.vscales = a.vscales;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
+  p.rope_theta = static_cast<double>(a.rope_theta);
+  p.out = a.out;
+  p.lse = a.lse;
+  p.prefix = reinterpret_cast<int64_t*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  p.epoch = next_epoch();
+  const int grid = 2 * n_sm < la::dpg::MAX_CTAS ? 2 * n_sm : la::dpg::MAX_CTAS;
+  constexpr uint32_t smem = la::dpg::Tile<kE4M3>::SMEM_ALLOC;
+  std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
+  prof_count(2);
+  const int pair = prof_before(stream);
+  if (G > 8)
+    la::dpg::decode_runs_kernel<kE4M3, kSparse, true><<<grid, la::dpg::NTHREADS, smem, stream>>>(tk, tv, p);
+  else
+    la::dpg::decode_runs_kernel<kE4M3, kSparse, false><<<grid, la::dpg::NTHREADS, smem, stream>>>(tk, tv, p);
+  const cudaError_t e = cudaGetLastError();
+  prof_after(pair, stream);
+  if (e != cudaSuccess) return LLAMA_ATTN_ERR_CUDA;
+  la::dpg::decode_join_kernel<kSparse><<<a.B * a.Hq, 128, 0, stream>>>(p, grid);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+extern "C" {
+
+int llama_attn_kv_append_paged(const llama_attn_bf16* k, const llama_attn_bf16* v, int64_t row_stride,
+                               int64_t batch_stride, llama_attn_bf16* kpages, llama_attn_bf16* vpages,
+                               llama_attn_bf16* kbounds, const int32_t* block_table, const int32_t* cache_lens,
+                               const int32_t* new_lens, int32_t* out_lens, int B, int T, int Hkv, int D, int page_size,
+                               int max_blocks, int n_pages, const void* rope_table, int rope_rows,
+                               cudaStream_t stream) {
+  return kv_append_paged<false>(AppendArgs{k, v, row_stride, batch_stride, kpages, vpages, nullptr, nullptr, kbounds,
+                                           block_table, cache_lens, new_lens, out_lens, B, T, Hkv, D, page_size,
+                                           max_blocks, n_pages, rope_table, rope_rows},
+                                stream);
+}
+
+int llama_attn_kv_append_paged_e4m3(const llama_attn_bf16* k, const llama_attn_bf16* v, int64_t row_stride,
+                                    int64_t batch_stride, uint8_t* kpages, uint8_t* vpages, float* k_scales,
+                                    float* v_scales, llama_attn_bf16* kbounds, const int32_t* block_table,
+                                    const int32_t* cache_lens, const int32_t* new_lens, int32_t* out_lens, int B,
+                                    int T, int Hkv, int D, int page_size, int max_blocks, int n_pages,
+                                    const void* rope_table, int rope_rows, cudaStream_t stream) {
+  return kv_append_paged<true>(AppendArgs{k, v, row_stride, batch_stride, kpages, vpages, k_scales, v_scales, kbounds,
+                                          block_table, cache_lens, new_lens, out_lens, B, T, Hkv, D, page_size,
+                                          max_blocks, n_pages, rope_table, rope_rows},
+                               stream);
+}
+
+size_t llama_attn_decode_runs_workspace_size(int B, int Hq, int Hkv, int D) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || D != 128 || Hq % Hkv != 0 || Hq / Hkv > 16) return 0;
+  return runs_ws_layout(B, Hq / Hkv).total;
+}
+
+int llama_attn_decode_paged_e4m3(const llama_attn_bf16* q, const uint8_t* kpages, const uint8_t* vpages,
+                                 const float* k_scales, const float* v_scales, const int32_t* block_table,
+                                 const int32_t* cache_lens, llama_attn_bf16* out, float* lse, int B, int Hq, int Hkv,
+                                 int D, int page_size, int max_blocks, int n_pages, int q_pos_offset,
+                                 float rope_theta, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return decode_runs<true, false>(RunsArgs{q, kpages, vpages, k_scales, v_scales, block_table, nullptr, cache_lens,
+                                           out, lse, B, Hq, Hkv, D, page_size, max_blocks, n_pages, 0, q_pos_offset,
+                                           rope_theta, workspace, workspace_bytes},
+                                  stream);
+}
+
+int llama_attn_decode_paged_sparse(const llama_attn_bf16* q, const llama_attn_bf16* kpages,
+                                   const llama_attn_bf16* vpages, const int32_t* block_table,
+                                   const int32_t* block_ids, const int32_t* cache_lens, llama_attn_bf16* out,
+                                   float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_blocks,
+                                   int n_pages, int n_sel, int q_pos_offset, float rope_theta, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+  return decode_runs<false, true>(RunsArgs{q, kpages, vpages, nullptr, nullptr, block_table, block_ids, cache_lens,
+                                           out, lse, B, Hq, Hkv, D, page_size, max_blocks, n_pages, n_sel,
+                                           q_pos_offset, rope_theta, workspace, workspace_bytes},
+                                  stream);
+}
+
+int llama_attn_decode_paged_sparse_e4m3(const llama_attn_bf16* q, const uint8_t* kpages, const uint8_t* vpages,
+                                        const float* k_scales, const float* v_scales, const int32_t* block_table,
+                                        const int32_t* block_ids, const int32_t* cache_lens, llama_attn_bf16* out,
+                                        float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_blocks,
+                                        int n_pages, int n_sel, int q_pos_offset, float rope_theta, void* workspace,
+                                        size_t workspace_bytes, cudaStream_t stream) {
+  return decode_runs<true, true>(RunsArgs{q, kpages, vpages, k_scales, v_scales, block_table, block_ids, cache_lens,
+                                          out, lse, B, Hq, Hkv, D, page_size, max_blocks, n_pages, n_sel,
+                                          q_pos_offset, rope_theta, workspace, workspace_bytes},
+                                 stream);
+}
+
+int llama_attn_select_blocks(const llama_attn_bf16* q, const llama_attn_bf16* kbounds, const int32_t* block_table,
+                             const int32_t* cache_lens, int32_t* block_ids, int B, int Hq, int Hkv, int D,
+                             int page_size, int max_blocks, int n_pages, int n_sel, int n_first, int n_last,
+                             int q_pos_offset, float rope_theta, cudaStream_t stream) {
+  if (!q || !kbounds || !block_table || !cache_lens || !block_ids) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (!(rope_theta > 0.f) || !std::isfinite(rope_theta)) return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (n_sel <= 0 || n_first < 0 || n_last < 0 || static_cast<int64_t>(n_first) + n_last > n_sel)
+    return LLAMA_ATTN_ERR_INVALID_ARG;
+  if (q_pos_offset != 0 && q_pos_offset != -1) return LLAMA_ATTN_ERR_INVALID_ARG;
+  int st = check_pages(B, Hkv, D, page_size, max_blocks, n_pages);
+  if (st) return st;
+  if (max_blocks > la::sel::MAX_BLOCKS || Hq > 65535) return LLAMA_ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(kbounds) || (reinterpret_cast<uintptr_t>(block_ids) & 3u))
+    return LLAMA_ATTN_ERR_INVALID_ARG;
+  int dev, n_sm = 148;
+  if ((st = current_device(&dev))) return st;
+  if ((st = device_setup(dev, &n_sm))) return st;
+  la::sel::Params p;
+  p.q = q;
+  p.kbounds = kbounds;
+  p.block_table = block_table;
+  p.lens = cache_lens;
+  p.ids = block_ids;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.page_size = page_size;
+  p.max_blocks = max_blocks;
+  p.n_pages = n_pages;
+  p.n_sel = n_sel;
+  p.n_first = n_first;
+  p.n_last = n_last;
+  p.q_pos_offset = q_pos_offset;
+  p.rope_theta = static_cast<double>(rope_theta);
+  // Clusters widen while the GPU has room for another CTA per pair and each
+  // would still have one pass (16 warps x 8 blocks) of its own.
+  const int64_t groups = static_cast<int64_t>(B) * Hkv;
+  int csize = 1;
+  while (csize < 8 && groups * csize * 2 <= 2 * n_sm && max_blocks > csize * la::sel::NWARPS * 8) csize *= 2;
+  if (groups * csize > INT32_MAX) return LLAMA_ATTN_ERR_UNSUPPORTED;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(groups * csize));
+  cfg.blockDim = dim3(la::sel::NTHREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(max_blocks) * 8;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
+  prof_count(1);
+  const int pair = prof_before(stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, la::sel::select_blocks_kernel, p);
+  prof_after(pair, stream);
+  return cuda_status(e);
 }
 
 }  // extern "C"

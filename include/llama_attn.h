@@ -367,6 +367,160 @@ int llama_attn_decode_noalloc(const llama_attn_bf16 *q, const llama_attn_bf16 *k
                               llama_attn_bf16 *out, int B, int Hq, int Hkv, int D, int Lmax,
                               float rope_theta, cudaStream_t stream);
 
+/*
+ * Paged KV cache: append, 8-bit decode and block-sparse decode
+ * ------------------------------------------------------------
+ * The calls below share llama_attn_decode_paged's cache (page pool, block
+ * table, lengths) and its limits: D == 128, page_size a multiple of 64, B and
+ * Hkv at most 65535, max_blocks * page_size and n_pages * Hkv * page_size below
+ * 2^31 rows (else LLAMA_ATTN_ERR_UNSUPPORTED). A "block" is one page's worth
+ * of consecutive rows of one sequence; block j of sequence b is page
+ * block_table[b * max_blocks + j]. Tensors are 16-byte aligned. None of the
+ * calls allocates or synchronises; each may be captured into a CUDA graph. Two
+ * calls whose kernels can overlap on the GPU must not share a workspace, nor
+ * write the same pages.
+ *
+ * E4M3 pages hold one code per value, [n_pages, Hkv, page_size, D], and one
+ * float32 scale per page and KV head, [n_pages, Hkv], for keys and for values:
+ * the value of a code is code * scale. A cache of this form takes half the
+ * bytes of bf16.
+ *
+ * The append writes new keys and values behind each sequence's rows, the keys
+ * rotated on the way at their cache positions (RoPE as for llama_attn_prefill):
+ *
+ *   k, v        [B, T, Hkv, D] un-rotated, token t of sequence b at element
+ *               b * batch_stride + t * row_stride (strides of both, in
+ *               elements, multiples of 8, row_stride >= Hkv * D): both may be
+ *               slices of a fused projection's rows
+ *   cache_lens  [B] int32: rows already in the cache
+ *   new_lens    [B] int32 in [0, T], or NULL for T: rows that sequence b gets;
+ *               rows past them in the padded batch are not read
+ *   kpages, vpages  the pool; row p of a sequence goes to row p % page_size of
+ *               block p / page_size. Rows at or past the new length are not
+ *               written, in a partly filled block neither. Entries of
+ *               block_table for the blocks that receive rows must be set; a
+ *               page belongs to one sequence of the call
+ *   kbounds     [n_pages, Hkv, 2, D] bf16 or NULL: the channel-wise least
+ *               ([.., 0, :]) and greatest ([.., 1, :]) rotated key of the
+ *               block's rows, for llama_attn_select_blocks. A block whose first
+ *               row is appended starts anew; otherwise the bounds there widen
+ *   out_lens    [B] int32 or NULL: cache_lens[b] + new_lens[b]; must not
+ *               overlap cache_lens
+ *   rope_table, rope_rows  a table from llama_attn_rope_table_build with at
+ *               least max_blocks * page_size rows
+ *   T >= 1.
+ * Keys are rotated in float32 (each product and the sum rounded once) and
+ * rounded once to the cache's type.
+ * _e4m3: a block's scale is 2^e with the least e in [-100, 119] for which its
+ * greatest magnitude is at most 448 * 2^e. When rows are appended to a partly
+ * filled block and they need a greater scale, the codes there are rounded
+ * again to it (exact but for values below 2^-6 of the new scale). k_scales and
+ * v_scales of a block whose first row is appended need no initialisation.
+ * NaN and infinite inputs give unspecified codes, scales and bounds in their
+ * own block.
+ * A length or a new length out of range sets LLAMA_ATTN_DEVERR_CACHE_LEN and
+ * that sequence is left as it was (out_lens[b] = cache_lens[b]); a page id
+ * outside [0, n_pages) sets LLAMA_ATTN_DEVERR_BLOCK_TABLE and that block's
+ * rows are not written.
+ */
+int llama_attn_kv_append_paged(const llama_attn_bf16 *k, const llama_attn_bf16 *v, int64_t row_stride,
+                               int64_t batch_stride, llama_attn_bf16 *kpages, llama_attn_bf16 *vpages,
+                               llama_attn_bf16 *kbounds, const int32_t *block_table,
+                               const int32_t *cache_lens, const int32_t *new_lens, int32_t *out_lens, int B,
+                               int T, int Hkv, int D, int page_size, int max_blocks, int n_pages,
+                               const void *rope_table, int rope_rows, cudaStream_t stream);
+int llama_attn_kv_append_paged_e4m3(const llama_attn_bf16 *k, const llama_attn_bf16 *v, int64_t row_stride,
+                                    int64_t batch_stride, uint8_t *kpages, uint8_t *vpages, float *k_scales,
+                                    float *v_scales, llama_attn_bf16 *kbounds, const int32_t *block_table,
+                                    const int32_t *cache_lens, const int32_t *new_lens, int32_t *out_lens,
+                                    int B, int T, int Hkv, int D, int page_size, int max_blocks,
+                                    int n_pages, const void *rope_table, int rope_rows, cudaStream_t stream);
+
+/*
+ * Bytes of device workspace of the three decode calls below (256-byte aligned;
+ * its contents need no initialisation): partial results of at most two
+ * (sequence, KV head) pairs per resident CTA, whatever the lengths are. 0 for
+ * invalid sizes.
+ */
+size_t llama_attn_decode_runs_workspace_size(int B, int Hq, int Hkv, int D);
+
+/*
+ * llama_attn_decode_paged against E4M3 pages:
+ * out = softmax(q . (k_code k_scale) / sqrt(D)) (v_code v_scale), the scales
+ * those of each row's page and KV head (any positive normal floats; those
+ * outside [2^-100, 2^119] for values are taken as the nearest of the two).
+ *
+ *   lse           [B, Hq] float32 or NULL: log sum_j exp(score_j), as for
+ *                 llama_attn_prefill_ex; -inf for a sequence without rows
+ *   q_pos_offset  the query of sequence b is rotated at position
+ *                 cache_lens[b] + q_pos_offset: 0 as in llama_attn_decode (its
+ *                 own key is not in the cache), -1 where it has been appended
+ *   out must not overlap q. Rows at or past cache_lens[b] are never used; a
+ *   sequence of length 0 gives out = 0.
+ * Codes of K and V are used exactly, scores, softmax sums and outputs are
+ * float32; q and the softmax weights are rounded to 11 bits. The result does
+ * not depend on timing. Errors and the other arguments as for
+ * llama_attn_decode_paged.
+ */
+int llama_attn_decode_paged_e4m3(const llama_attn_bf16 *q, const uint8_t *kpages, const uint8_t *vpages,
+                                 const float *k_scales, const float *v_scales, const int32_t *block_table,
+                                 const int32_t *cache_lens, llama_attn_bf16 *out, float *lse, int B, int Hq,
+                                 int Hkv, int D, int page_size, int max_blocks, int n_pages,
+                                 int q_pos_offset, float rope_theta, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Chooses the blocks that a decode should read, per sequence and KV head:
+ * block j scores sum over the query heads h of the KV group of
+ * sum_d max(q_hd lo_jd, q_hd hi_jd), an upper bound of the summed products of
+ * the rotated queries with any key of the block (lo, hi: its kbounds),
+ * computed in float64.
+ *
+ *   q          [B, Hq, D] un-rotated, rotated at cache_lens[b] + q_pos_offset
+ *   kbounds    [n_pages, Hkv, 2, D] bf16, as llama_attn_kv_append_paged writes it
+ *   block_ids  [B, Hkv, n_sel] int32 out: the first n_first and the last
+ *              n_last blocks of the sequence, and of the others those with the
+ *              greatest scores (of equal scores the lower index), n_sel in
+ *              all, ascending; every block, then -1, where the sequence has
+ *              at most n_sel
+ *   n_sel >= 1, n_first, n_last >= 0, n_first + n_last <= n_sel;
+ *   max_blocks <= 24576 (else LLAMA_ATTN_ERR_UNSUPPORTED).
+ * A page id outside [0, n_pages) sets LLAMA_ATTN_DEVERR_BLOCK_TABLE and its
+ * block scores 0; a length outside [0, max_blocks * page_size] sets
+ * LLAMA_ATTN_DEVERR_CACHE_LEN and the ids are -1. A NaN score counts as the
+ * greatest.
+ */
+int llama_attn_select_blocks(const llama_attn_bf16 *q, const llama_attn_bf16 *kbounds,
+                             const int32_t *block_table, const int32_t *cache_lens, int32_t *block_ids,
+                             int B, int Hq, int Hkv, int D, int page_size, int max_blocks, int n_pages,
+                             int n_sel, int n_first, int n_last, int q_pos_offset, float rope_theta,
+                             cudaStream_t stream);
+
+/*
+ * Decode over chosen blocks: the query heads of KV head g of sequence b attend
+ * to the rows below cache_lens[b] of blocks block_ids[b, g, :] and to no
+ * others. The ids are ascending, each at most once, below the sequence's
+ * number of blocks, with -1 behind the last one; entries past the sequence's
+ * number of blocks are not read. An entry that breaks this sets
+ * LLAMA_ATTN_DEVERR_BLOCK_IDS and contributes nothing; the output is then
+ * unspecified. No id: out = 0, lse = -inf. Other arguments and errors as for
+ * llama_attn_decode_paged_e4m3. On bf16 pages the softmax weights are rounded
+ * to bf16 and q to 17 bits.
+ */
+int llama_attn_decode_paged_sparse(const llama_attn_bf16 *q, const llama_attn_bf16 *kpages,
+                                   const llama_attn_bf16 *vpages, const int32_t *block_table,
+                                   const int32_t *block_ids, const int32_t *cache_lens, llama_attn_bf16 *out,
+                                   float *lse, int B, int Hq, int Hkv, int D, int page_size, int max_blocks,
+                                   int n_pages, int n_sel, int q_pos_offset, float rope_theta,
+                                   void *workspace, size_t workspace_bytes, cudaStream_t stream);
+int llama_attn_decode_paged_sparse_e4m3(const llama_attn_bf16 *q, const uint8_t *kpages,
+                                        const uint8_t *vpages, const float *k_scales, const float *v_scales,
+                                        const int32_t *block_table, const int32_t *block_ids,
+                                        const int32_t *cache_lens, llama_attn_bf16 *out, float *lse, int B,
+                                        int Hq, int Hkv, int D, int page_size, int max_blocks, int n_pages,
+                                        int n_sel, int q_pos_offset, float rope_theta, void *workspace,
+                                        size_t workspace_bytes, cudaStream_t stream);
+
 /* Static, human-readable text for a status code. Never NULL. */
 const char *llama_attn_status_string(int status);
 
@@ -375,6 +529,7 @@ const char *llama_attn_status_string(int status);
 #define LLAMA_ATTN_DEVERR_DOC_OFFSETS 0x2 /* malformed doc_offsets */
 #define LLAMA_ATTN_DEVERR_CACHE_LEN 0x4   /* cache_lens[b] outside [0, Lmax] */
 #define LLAMA_ATTN_DEVERR_BLOCK_TABLE 0x8 /* a paged-cache block id outside [0, n_pages) */
+#define LLAMA_ATTN_DEVERR_BLOCK_IDS 0x10  /* block_ids not ascending, or past the sequence's last block */
 
 /*
  * Waits for `stream`, then returns and clears the current device's error word

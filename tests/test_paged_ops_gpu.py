@@ -1,0 +1,612 @@
+"""GPU parity of the paged-cache operators (append with rotation into bf16 and
+E4M3 pages, decode over E4M3 pages, block selection, block-sparse decode)
+against their float64 statements in paged_reference.py.
+
+Tolerances, derived before the first run (u: half a step of a type, relative:
+bf16 2^-8, f16 2^-11, float32 2^-24, E4M3 2^-4 or 2^-10 absolute below 2^-6):
+
+* appended bf16 rows: one bf16 rounding, u |x|, and the float32 rotation: two
+  products, a sum and the table's rounding, at most 4 u32 (|x0| + |x1|);
+* appended E4M3 rows: one E4M3 rounding of x / scale, plus the same rotation
+  error; scales and re-coded older rows exactly;
+* attention over E4M3 pages: q carries 1 f16 rounding, so a score is off by at
+  most delta = 2^-11 S + 2^-19 (1 + |s|), S = sum_d |q_d k_d| / sqrt(D), and a
+  softmax weight by the factor e^(2 delta); the weight itself is rounded to f16
+  (2^-11, and 2^-25 of 2^7 absolute: 2^-32 for each of n rows); then one bf16
+  rounding of the output. With A = sum_n p_n |v_n|:
+  |err| <= u |out| + A (expm1(2 delta) + 2^-10) + n 2^-32 max|v|;
+* over bf16 pages: q carries 2^-17 (two bf16 terms), a weight 2^-8.
+* the log-sum-exp: delta, and float32 rounding.
+The 2^-19 (1 + |s|) covers float32 sums of 128 products (their errors are far
+below the worst case) and the exponent's and exponential's own rounding.
+"""
+import math
+
+import pytest
+import torch
+
+import gqa_attention_rope_b200 as la
+import paged_reference as R
+from gqa_attention_rope_b200 import build as labuild
+from guards import check_guard, guarded
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+THETA = 500000.0
+U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    labuild.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    la.lib()
+    la.llama_attn_get_device_error()
+    yield
+    assert la.llama_attn_get_device_error() == 0
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def make_table(g, lens, page, extra=2, slack=0):
+    """A block table whose pages lie scattered in the pool; unset entries are -1."""
+    need = [-(-n // page) for n in lens]
+    blocks = max(1, max(need)) + slack
+    n_pages = sum(need) + extra
+    perm = torch.randperm(n_pages, generator=g).to(torch.int32)
+    table = torch.full((len(lens), blocks), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    return table, n_pages
+
+
+def e4m3_pool(g, n_pages, Hkv, page, spread=0):
+    """Random codes without NaN, and scales 2^-spread .. 2^spread."""
+    x = (torch.randn(n_pages, Hkv, page, D, generator=g) * 64).clamp(-448, 448)
+    e = torch.randint(-spread, spread + 1, (n_pages, Hkv), generator=g)
+    return x.to(torch.float8_e4m3fn).view(torch.uint8), torch.ldexp(torch.full((n_pages, Hkv), 1 / 64), e)
+
+
+def poison_tails(pools, table, lens, page, value):
+    """Rows at or past each sequence's length, and pages of no sequence, hold ``value``."""
+    for pool in pools:
+        used = torch.zeros(pool.shape[0], dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for j in range(-(-n // page)):
+                pg = int(table[b, j])
+                used[pg] = True
+                pool[pg, :, max(0, n - j * page):] = value
+        pool[~used] = value
+
+
+# ---------------------------------------------------------------- append
+APPEND = [
+    # kind, page, Hkv, T, lens, new_lens (None: all T)
+    ("bf16", 64, 2, 1, [0, 1, 63, 64, 200], None),
+    ("e4m3", 64, 2, 1, [0, 1, 63, 64, 200], None),
+    ("bf16", 64, 1, 130, [0, 5, 64], None),
+    ("e4m3", 64, 1, 130, [0, 5, 64], None),
+    ("e4m3", 64, 8, 17, [60, 0, 47], [17, 0, 3]),
+    ("bf16", 192, 3, 200, [100, 191], [200, 1]),
+    ("e4m3", 192, 3, 401, [100, 191, 0], [401, 1, 0]),
+    ("e4m3", 256, 2, 300, [0, 255], None),
+    ("e4m3", 1024, 1, 1500, [700], None),
+]
+
+
+def append_state(kind, page, Hkv, T, lens, new_lens, seed):
+    g = gen(seed)
+    B = len(lens)
+    new = list(new_lens) if new_lens else [T] * B
+    table, n_pages = make_table(g, [n + t for n, t in zip(lens, new)], page)
+    if kind == "bf16":
+        pools = [torch.randn(n_pages, Hkv, page, D, generator=g).to(torch.bfloat16) for _ in range(2)]
+        scales = None
+    else:
+        pools, scales = zip(*(e4m3_pool(g, n_pages, Hkv, page, 3) for _ in range(2)))
+        pools, scales = list(pools), list(scales)
+    bounds = torch.randn(n_pages, Hkv, 2, D, generator=g).sort(dim=2).values.to(torch.bfloat16)
+    k, v = (torch.randn(B, T, Hkv, D, generator=g).mul(3).to(torch.bfloat16) for _ in range(2))
+    for b in range(B):  # rows past new_lens are not read
+        k[b, new[b]:] = math.nan
+        v[b, new[b]:] = math.nan
+    return dict(B=B, new=new, table=table, n_pages=n_pages, pools=pools, scales=scales, bounds=bounds, k=k, v=v)
+
+
+def run_append(kind, s, lens, rope, k, v, new_lens, bounds=True, **kw):
+    d = dict(pools=[p.cuda() for p in s["pools"]],
+             scales=[x.cuda() for x in s["scales"]] if s["scales"] else [],
+             bounds=s["bounds"].cuda() if bounds else None,
+             out_lens=torch.full((s["B"],), -7, dtype=torch.int32, device="cuda"))
+    fn = la.llama_attn_kv_append_paged if kind == "bf16" else la.llama_attn_kv_append_paged_e4m3
+    got = fn(k, v, *d["pools"], *d["scales"], s["table"].cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+             rope, new_lens=torch.tensor(new_lens, dtype=torch.int32, device="cuda") if new_lens else None,
+             kbounds=d["bounds"], out_lens=d["out_lens"], **kw)
+    assert got is d["out_lens"]
+    return d
+
+
+@pytest.mark.parametrize("kind,page,Hkv,T,lens,new_lens", APPEND)
+def test_append(kind, page, Hkv, T, lens, new_lens):
+    s = append_state(kind, page, Hkv, T, lens, new_lens, 11 + T)
+    rope = la.llama_attn_rope_table_build(s["table"].shape[1] * page, D, THETA)
+    d = run_append(kind, s, lens, rope, s["k"].cuda(), s["v"].cuda(), new_lens)
+    torch.cuda.synchronize()
+    assert d["out_lens"].tolist() == [n + t for n, t in zip(lens, s["new"])]
+    value = (lambda p: p.double()) if kind == "bf16" else R.codes
+    ref_pools = [value(p).clone() for p in s["pools"]]
+    ref_scales = [x.double().clone() for x in s["scales"]] if s["scales"] else None
+    ref_bounds = s["bounds"].double().clone()
+    R.append(s["k"], s["v"], ref_pools, ref_scales, ref_bounds, s["table"], lens, s["new"], page, THETA)
+    written = torch.zeros(s["n_pages"], page, dtype=torch.bool)
+    mag = torch.zeros(s["n_pages"], Hkv, page, D, dtype=torch.float64)  # |x0| + |x1| of each written key
+    for b in range(s["B"]):
+        for t in range(s["new"][b]):
+            p = lens[b] + t
+            pg = int(s["table"][b, p // page])
+            written[pg, p % page] = True
+            x = s["k"][b, t].double().abs().view(Hkv, D // 2, 2).sum(-1, keepdim=True).expand(-1, -1, 2)
+            mag[pg, :, p % page] = x.reshape(Hkv, D)
+    for c in (0, 1):
+        got, ref = value(d["pools"][c].cpu()), ref_pools[c]
+        rot = 4 * U["f32"] * mag if c == 0 else torch.zeros_like(mag)
+        if kind == "e4m3":
+            assert torch.equal(d["scales"][c].cpu().double(), ref_scales[c]), "scales"
+            tol = torch.maximum(2.0 ** -4 * ref.abs(), torch.tensor(2.0 ** -10, dtype=torch.float64)) \
+                + 1.07 * rot / ref_scales[c][:, :, None, None]
+        else:
+            tol = U["bf16"] * ref.abs() + 1.01 * rot
+        w = written[:, None, :, None]
+        assert torch.all(((got - ref).abs() <= tol) | ~w), "appended rows"
+        assert torch.equal(torch.where(w, 0.0, got), torch.where(w, 0.0, ref)), "other rows"
+        if kind == "bf16":
+            raw, was = d["pools"][c].cpu().view(torch.int16), s["pools"][c].view(torch.int16)
+            assert torch.equal(torch.where(w, 0, raw), torch.where(w, 0, was)), "other rows' bits"
+    got = d["bounds"].cpu().double()
+    top = 3 * 8.0  # |x0| + |x1| of any key here
+    assert torch.all((got - ref_bounds).abs() <= U["bf16"] * ref_bounds.abs() + 4 * U["f32"] * top)
+
+
+def test_append_without_bounds_and_with_fused_projection_strides():
+    """k and v as slices of a fused [B, T, (Hq + 2 Hkv) * D] projection, also of a longer batch."""
+    page, Hkv, Hq, T, lens = 64, 2, 4, 70, [3, 64]
+    s = append_state("e4m3", page, Hkv, T, lens, None, 5)
+    W = (Hq + 2 * Hkv) * D
+    fused = torch.full((2, T + 9, W), math.nan, dtype=torch.bfloat16)
+    fused[:, :T, Hq * D:(Hq + Hkv) * D] = s["k"].reshape(2, T, -1)
+    fused[:, :T, (Hq + Hkv) * D:] = s["v"].reshape(2, T, -1)
+    f = fused.cuda()
+    k = f[:, :T, Hq * D:(Hq + Hkv) * D].view(2, T, Hkv, D)
+    v = f[:, :T, (Hq + Hkv) * D:].view(2, T, Hkv, D)
+    rope = la.llama_attn_rope_table_build(s["table"].shape[1] * page, D, THETA)
+    a = run_append("e4m3", s, lens, rope, k, v, None, bounds=False)
+    b = run_append("e4m3", s, lens, rope, s["k"].cuda(), s["v"].cuda(), None)
+    for x, y in zip(a["pools"] + a["scales"], b["pools"] + b["scales"]):
+        assert torch.equal(x, y)
+    # one prompt for every sequence of the batch: batch stride 0
+    c = run_append("e4m3", s, lens, rope, k[:1].expand(2, -1, -1, -1), v[:1].expand(2, -1, -1, -1), None)
+    e = run_append("e4m3", s, lens, rope, k[:1].repeat(2, 1, 1, 1), v[:1].repeat(2, 1, 1, 1), None)
+    for x, y in zip(c["pools"] + c["scales"], e["pools"] + e["scales"]):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("T", [1, 7, 64])
+def test_append_steps_equal_one_append_but_for_subnormals(T):
+    """An E4M3 block filled T rows at a time: same scales as at once; codes differ at most by
+    the second rounding of values below 2^-6 of the final scale (half a subnormal step)."""
+    page, Hkv, n = 64, 2, 64
+    g = gen(77)
+    k, v = ((torch.randn(1, n, Hkv, D, generator=g) * torch.logspace(-3, 3, n, base=2)[None, :, None, None])
+            .to(torch.bfloat16).cuda() for _ in range(2))
+    rope = la.llama_attn_rope_table_build(page, D, THETA)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+
+    def fresh():
+        return ([torch.zeros(1, Hkv, page, D, dtype=torch.uint8, device="cuda") for _ in range(2)],
+                [torch.full((1, Hkv), math.nan, device="cuda") for _ in range(2)],
+                torch.full((1, Hkv, 2, D), math.nan, dtype=torch.bfloat16, device="cuda"))
+    p1, s1, b1 = fresh()
+    la.llama_attn_kv_append_paged_e4m3(k, v, *p1, *s1, table, torch.zeros(1, dtype=torch.int32, device="cuda"), rope,
+                                       kbounds=b1)
+    p2, s2, b2 = fresh()
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for t in range(0, n, T):
+        nxt = torch.empty_like(lens)
+        la.llama_attn_kv_append_paged_e4m3(k[:, t:t + T], v[:, t:t + T], *p2, *s2, table, lens, rope, kbounds=b2,
+                                           out_lens=nxt)
+        lens = nxt
+    torch.cuda.synchronize()
+    assert lens.item() == n and torch.equal(b1, b2)
+    for x, y, sx, sy in zip(p1, p2, s1, s2):
+        assert torch.equal(sx, sy)
+        x, y = R.codes(x.cpu()), R.codes(y.cpu())
+        big = x.abs() >= 2.0 ** -5
+        assert torch.equal(x[big], y[big])
+        assert (x - y).abs().max() <= 2.0 ** -9  # two roundings, half a subnormal step each
+
+
+def test_append_leaves_refused_sequences_alone():
+    page, Hkv, T = 64, 1, 4
+    lens, new = [-1, 10, 126, 5], [4, 9, 4, 4]  # negative length, more than T, past the table, fine
+    s = append_state("bf16", page, Hkv, T, [0, 0, 0, 5], [4, 4, 4, 4], 3)
+    s["table"] = torch.tensor([[0, 1], [2, 3], [4, 5], [1, 9]], dtype=torch.int32)
+    s["pools"] = [torch.randn(6, Hkv, page, D).to(torch.bfloat16) for _ in range(2)]
+    s["bounds"] = torch.zeros(6, Hkv, 2, D, dtype=torch.bfloat16)
+    rope = la.llama_attn_rope_table_build(2 * page, D, THETA)
+    d = run_append("bf16", s, lens, rope, s["k"].cuda(), s["v"].cuda(), new)
+    assert la.llama_attn_get_device_error() == la.DEVERR_CACHE_LEN
+    assert d["out_lens"].tolist() == [-1, 10, 126, 9]
+    keep = [0, 2, 3, 4, 5]
+    for x, y in zip(d["pools"], s["pools"]):
+        assert torch.equal(x.cpu()[keep], y[keep]) and not torch.equal(x.cpu()[1], y[1])
+    s["table"][3, 0] = 6  # a page that is not there
+    d = run_append("bf16", s, [0, 0, 0, 5], rope, s["k"].cuda().nan_to_num(), s["v"].cuda().nan_to_num(), [0, 0, 0, 4])
+    assert la.llama_attn_get_device_error() == la.DEVERR_BLOCK_TABLE
+    for x, y in zip(d["pools"], s["pools"]):
+        assert torch.equal(x.cpu(), y)
+
+
+# ---------------------------------------------------------------- attention
+def check_attention(kind, out, lse, ref, max_v, n_rows):
+    o, ref_lse, mass, span = ref
+    u_q, u_p = (2.0 ** -11, 2.0 ** -10) if kind == "e4m3" else (2.0 ** -17, 2.0 ** -8)
+    live = torch.isfinite(ref_lse)
+    s_abs = torch.where(live, ref_lse.abs(), 0.0) + span  # |s| <= S; the exponent's reference is near the lse
+    delta = u_q * span + 2.0 ** -19 * (1 + s_abs)
+    tol = U["bf16"] * o.abs() + mass * (torch.expm1(2 * delta) + u_p)[..., None] + n_rows * 2.0 ** -32 * max_v
+    err = (out.double().cpu() - o).abs()
+    assert torch.all(err <= tol), f"worst error over tolerance: {(err / tol.clamp(min=1e-30)).max():.3g}"
+    if lse is not None:
+        got = lse.double().cpu()
+        assert torch.equal(torch.isinf(got), ~live)
+        assert torch.all((got - ref_lse)[live].abs() <= (delta + 2.0 ** -22 * (1 + s_abs))[live])
+
+
+def attention_state(kind, page, Hq, Hkv, lens, seed, spread=0, q_scale=2.0):
+    g = gen(seed)
+    table, n_pages = make_table(g, lens, page, slack=1)
+    if kind == "e4m3":
+        (kp, ks), (vp, vs) = (e4m3_pool(g, n_pages, Hkv, page, spread if c else 0) for c in (0, 1))
+        poison_tails([kp, vp], table, lens, page, 0x7F)
+        kv = R.codes(kp) * ks.double()[:, :, None, None]
+        vv = R.codes(vp) * vs.double()[:, :, None, None]
+        scales = [ks, vs]
+    else:
+        kp, vp = (torch.randn(n_pages, Hkv, page, D, generator=g).to(torch.bfloat16) for _ in range(2))
+        poison_tails([kp, vp], table, lens, page, math.nan)
+        kv, vv, scales = kp.double(), vp.double(), []
+    q = (torch.randn(len(lens), Hq, D, generator=g) * q_scale).to(torch.bfloat16)
+    return dict(q=q, kp=kp, vp=vp, kv=kv, vv=vv, scales=scales, table=table, lens=lens, page=page)
+
+
+def on_gpu(s):
+    return dict(q=s["q"].cuda(), pools=(s["kp"].cuda(), s["vp"].cuda()), scales=tuple(x.cuda() for x in s["scales"]),
+                table=s["table"].cuda(), lens=torch.tensor(s["lens"], dtype=torch.int32, device="cuda"))
+
+
+DECODE = [
+    # page, Hq, Hkv, lens, spread of the value scales, q_pos_offset
+    (64, 32, 8, [1000], 0, 0),
+    (64, 8, 1, [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 640], 0, 0),
+    (128, 1, 1, [300, 5], 2, -1),
+    (256, 6, 2, [256, 255, 257, 0, 1], 4, 0),
+    (64, 10, 2, [777, 64], 0, -1),
+    (192, 18, 2, [500, 191, 193], 3, 0),
+    (64, 32, 2, [2049, 1, 63], 0, 0),
+    (64, 13, 13, [90, 200], 0, 0),
+    (128, 16, 1, [20000], 1, 0),
+]
+
+
+@pytest.mark.parametrize("page,Hq,Hkv,lens,spread,off", DECODE)
+def test_decode_e4m3(page, Hq, Hkv, lens, spread, off):
+    s = attention_state("e4m3", page, Hq, Hkv, lens, 100 + Hq + page, spread)
+    d = on_gpu(s)
+    buf, out = guarded(s["q"].shape)
+    lse = torch.empty(len(lens), Hq, device="cuda")
+    ws = torch.full((la.llama_attn_decode_runs_workspace_size(len(lens), Hq, Hkv),), 0xAB, dtype=torch.uint8,
+                    device="cuda")
+    got = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], out=out, lse=lse,
+                                          workspace=ws, q_pos_offset=off)
+    assert got is out
+    torch.cuda.synchronize()
+    check_guard(buf)
+    ref = R.decode(s["q"], s["kv"], s["vv"], s["table"], lens, page, THETA, off)
+    max_v = max(float(s["vv"][s["table"][b, j].long()].nan_to_num().abs().max())
+                for b, n in enumerate(lens) for j in range(-(-n // page)))
+    check_attention("e4m3", out, lse, ref, max_v, max(lens))
+    again = la.llama_attn_decode_paged_e4m3(d["q"], d["pools"][0].view(torch.float8_e4m3fn),
+                                            d["pools"][1].view(torch.float8_e4m3fn), *d["scales"], d["table"],
+                                            d["lens"], q_pos_offset=off)
+    assert torch.equal(again, out), "a second call, its own workspace, no lse"
+
+
+@pytest.mark.parametrize("scale_k,scale_v", [(0.0173, 0.31), (2.0 ** -40, 2.0 ** 90), (3.0e-3, 2.0 ** -95)])
+def test_decode_e4m3_any_positive_scale(scale_k, scale_v):
+    s = attention_state("e4m3", 64, 8, 2, [130, 64], 9)
+    for c, x in enumerate((scale_k, scale_v)):
+        s["scales"][c] = (torch.rand(s["scales"][c].shape, generator=gen(c)) + 0.5) * x
+    s["kv"] = R.codes(s["kp"]) * s["scales"][0].double()[:, :, None, None]
+    s["vv"] = R.codes(s["vp"]) * s["scales"][1].double()[:, :, None, None]
+    d = on_gpu(s)
+    lse = torch.empty(2, 8, device="cuda")
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], lse=lse)
+    check_attention("e4m3", out, lse, R.decode(s["q"], s["kv"], s["vv"], s["table"], s["lens"], 64, THETA),
+                    448 * 1.5 * scale_v, 130)
+
+
+@pytest.mark.parametrize("q_scale", [1e-30, 1e30, 40.0])
+def test_decode_e4m3_query_magnitudes(q_scale):
+    """Queries far outside f16's range (1e30: the greatest key takes all the weight)."""
+    s = attention_state("e4m3", 64, 4, 1, [100], 21, q_scale=q_scale)
+    if q_scale == 1e30:  # one key per head stands out, so that rounding cannot change the winner
+        s["q"] = (torch.sign(s["q"].double()) * 1e30).to(torch.bfloat16)
+        s["kp"][s["table"][0].clamp(min=0).long()] &= 0x80  # +-0 but for one row
+        s["kp"][int(s["table"][0, 0]), 0, 7] = 0x38 | (s["kp"][int(s["table"][0, 0]), 0, 7] & 0x80)
+        s["kv"] = R.codes(s["kp"]) * s["scales"][0].double()[:, :, None, None]
+    d = on_gpu(s)
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"])
+    o, l, mass, span = R.decode(s["q"], s["kv"], s["vv"], s["table"], s["lens"], 64, THETA)
+    if q_scale == 1e30:
+        assert torch.all((out.double().cpu() - o).abs() <= U["bf16"] * o.abs() + 2.0 ** -10 * mass)
+    else:
+        check_attention("e4m3", out, None, (o, l, mass, span), 448 / 64, 100)
+
+
+SPARSE = [
+    # kind, page, Hq, Hkv, lens, n_sel, n_first, n_last, q_pos_offset
+    ("bf16", 64, 8, 2, [0, 1, 64, 65, 1000, 3000], 7, 1, 1, 0),
+    ("e4m3", 64, 8, 2, [0, 1, 64, 65, 1000, 3000], 7, 1, 1, 0),
+    ("bf16", 128, 32, 2, [5000, 129], 5, 0, 2, -1),
+    ("e4m3", 256, 9, 1, [4000, 256, 4097], 3, 1, 2, 0),
+    ("bf16", 64, 1, 1, [777], 1, 0, 0, 0),
+    ("e4m3", 192, 12, 12, [1000, 10], 40, 1, 1, -1),
+    ("e4m3", 64, 16, 1, [70001], 128, 4, 4, 0),
+    ("bf16", 64, 4, 4, [20011, 9000], 33, 1, 0, 0),
+]
+
+
+def bounds_of(s, value=None):
+    lo, hi = s["kv"].nan_to_num(nan=math.inf).amin(2), s["kv"].nan_to_num(nan=-math.inf).amax(2)
+    return torch.stack([lo, hi], 2).clamp(-1e30, 1e30).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind,page,Hq,Hkv,lens,n_sel,n_first,n_last,off", SPARSE)
+def test_select_and_sparse_decode(kind, page, Hq, Hkv, lens, n_sel, n_first, n_last, off):
+    s = attention_state(kind, page, Hq, Hkv, lens, 300 + Hq + page)
+    d = on_gpu(s)
+    bounds = bounds_of(s)
+    buf, ids = guarded((len(lens), Hkv, n_sel), torch.int32, 12345)
+    got = la.llama_attn_select_blocks(d["q"], bounds.cuda(), d["table"], d["lens"], page, n_sel, n_first, n_last,
+                                      block_ids=ids, q_pos_offset=off)
+    assert got is ids
+    torch.cuda.synchronize()
+    check_guard(buf, 12345, "block_ids")
+    ref_ids = R.select(s["q"], bounds, s["table"], lens, page, n_sel, n_first, n_last, THETA, off)
+    assert torch.equal(ids.cpu(), ref_ids)
+    fn = la.llama_attn_decode_paged_sparse if kind == "bf16" else la.llama_attn_decode_paged_sparse_e4m3
+    buf, out = guarded(s["q"].shape)
+    lse = torch.empty(len(lens), Hq, device="cuda")
+    fn(d["q"], *d["pools"], *d["scales"], d["table"], ids, d["lens"], out=out, lse=lse, q_pos_offset=off)
+    torch.cuda.synchronize()
+    check_guard(buf)
+    ref = R.decode(s["q"], s["kv"], s["vv"], s["table"], lens, page, THETA, off, ref_ids)
+    check_attention(kind, out, lse, ref, 8.0, n_sel * page)
+
+
+def test_select_ties_and_equal_scores():
+    """Equal blocks: the lowest indices; two values only: all of the greater, then the lowest others."""
+    Hq, Hkv, page, nb = 4, 1, 64, 300
+    q = torch.randn(1, Hq, D, generator=gen(1)).to(torch.bfloat16)
+    table = torch.randperm(nb, generator=gen(2)).to(torch.int32)[None]
+    lens = torch.tensor([nb * page], dtype=torch.int32)
+    for greater in ([], [7, 100, 298], list(range(40, 90))):
+        bounds = torch.ones(nb, Hkv, 2, D, dtype=torch.bfloat16)
+        bounds[:, :, 0] = -1
+        for j in greater:
+            bounds[table[0, j].long()] *= 2
+        ids = la.llama_attn_select_blocks(q.cuda(), bounds.cuda(), table.cuda(), lens.cuda(), page, 20, 2, 1)
+        best = (greater + [j for j in range(2, nb - 1) if j not in greater])[:17]
+        assert ids[0, 0].tolist() == sorted([0, 1] + best + [nb - 1])
+
+
+@pytest.mark.parametrize("B,Hkv,nb", [(1, 1, 2048), (1, 8, 1000), (40, 8, 129), (2, 2, 24576)])
+def test_select_cluster_sizes(B, Hkv, nb):
+    """Every cluster width, up to the greatest number of blocks."""
+    page, Hq, n_sel = 64, Hkv, 50
+    g = gen(nb)
+    q = torch.randn(B, Hq, D, generator=g).to(torch.bfloat16)
+    n_pages = 256
+    bounds = torch.randn(n_pages, Hkv, 2, D, generator=g).sort(dim=2).values.to(torch.bfloat16)
+    table = torch.randint(0, n_pages, (B, nb), generator=g, dtype=torch.int32)  # pages shared: many ties
+    lens = [nb * page - 63 * (b % 2) for b in range(B)]
+    ids = la.llama_attn_select_blocks(q.cuda(), bounds.cuda(), table.cuda(),
+                                      torch.tensor(lens, dtype=torch.int32, device="cuda"), page, n_sel)
+    assert torch.equal(ids.cpu(), R.select(q, bounds, table, lens, page, n_sel, 1, 1, THETA))
+
+
+def test_sparse_over_all_blocks_matches_dense_and_paged_decode():
+    """Every block chosen: the E4M3 forms agree bit for bit (same units), bf16 with the bf16 decode."""
+    s = attention_state("e4m3", 64, 16, 2, [700, 64, 1], 31)
+    d = on_gpu(s)
+    ids = torch.full((3, 2, 11), -1, dtype=torch.int32)
+    for b, n in enumerate(s["lens"]):
+        ids[b, :, :-(-n // 64)] = torch.arange(-(-n // 64))
+    a = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"])
+    b = la.llama_attn_decode_paged_sparse_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], ids.cuda(), d["lens"])
+    assert torch.equal(a, b)
+    s = attention_state("bf16", 64, 16, 2, [700, 64, 1], 32)
+    d = on_gpu(s)
+    a = la.llama_attn_decode_paged(d["q"], *d["pools"], d["table"], d["lens"])
+    b = la.llama_attn_decode_paged_sparse(d["q"], *d["pools"], d["table"], ids.cuda(), d["lens"])
+    assert (a.float() - b.float()).abs().max() <= 1.5e-2  # the bf16 decode's own tolerance
+
+
+def test_sparse_ids_are_checked_on_the_device():
+    s = attention_state("bf16", 64, 4, 1, [200], 41)
+    d = on_gpu(s)
+
+    def run(ids):
+        out = la.llama_attn_decode_paged_sparse(d["q"], *d["pools"], d["table"],
+                                                torch.tensor([[ids]], dtype=torch.int32, device="cuda"), d["lens"])
+        return la.llama_attn_get_device_error(), out
+    for bad in ([2, 1, -1, -1], [1, 1, -1, -1], [-1, 2, -1, -1], [0, 4, -1, -1], [-5, -1, -1, -1], [0, 1 << 30, -1, -1]):
+        err, out = run(bad)
+        assert err == la.DEVERR_BLOCK_IDS, bad
+        assert torch.isfinite(out.float()).all()
+    err, out = run([-1, -1, -1, -1])
+    assert err == 0 and not out.any()
+    err, out = run([0, 2, 3, -1, 99, 99])  # entries past the sequence's number of blocks are not read
+    assert err == 0
+    ref = R.decode(s["q"], s["kv"], s["vv"], s["table"], s["lens"], 64, THETA, 0, torch.tensor([[[0, 2, 3]]]))
+    check_attention("bf16", out, None, ref, 8.0, 200)
+
+
+def test_bad_pages_and_lengths_set_the_error_word():
+    s = attention_state("e4m3", 64, 4, 1, [100, 100, 100], 51)
+    d = on_gpu(s)
+    table = d["table"].clone()
+    table[0, 1] = s["kp"].shape[0]
+    lens = torch.tensor([100, -3, 64 * table.shape[1] + 1], dtype=torch.int32, device="cuda")
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], table, lens)
+    assert la.llama_attn_get_device_error() == la.DEVERR_BLOCK_TABLE | la.DEVERR_CACHE_LEN
+    assert torch.isfinite(out.float()).all() and not out[1:].any()
+    bounds = torch.zeros(s["kp"].shape[0], 1, 2, D, dtype=torch.bfloat16, device="cuda")
+    ids = la.llama_attn_select_blocks(d["q"], bounds, table, lens, 64, 1, 0, 0)
+    assert la.llama_attn_get_device_error() == la.DEVERR_BLOCK_TABLE | la.DEVERR_CACHE_LEN
+    assert ids[1:].eq(-1).all()
+
+
+# ---------------------------------------------------------------- used as a program uses them
+def test_serving_loop_prompt_then_steps():
+    """A prompt is appended to E4M3 pages, then tokens one by one: append, choose blocks, attend
+    with the token's own key in the cache. The cache and every step against float64."""
+    page, Hq, Hkv, steps = 64, 8, 2, 5
+    prompt = [150, 1, 64]
+    B = len(prompt)
+    g = gen(61)
+    T = max(prompt)
+    k, v = (torch.randn(B, T, Hkv, D, generator=g).to(torch.bfloat16) for _ in range(2))
+    total = [n + steps for n in prompt]
+    table, n_pages = make_table(g, total, page)
+    rope = la.llama_attn_rope_table_build(table.shape[1] * page, D, THETA)
+    kp, vp = (torch.full((n_pages, Hkv, page, D), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((n_pages, Hkv), math.nan, device="cuda") for _ in range(2))
+    kb = torch.full((n_pages, Hkv, 2, D), math.nan, dtype=torch.bfloat16, device="cuda")
+    dt = table.cuda()
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    after = torch.empty_like(lens)
+    la.llama_attn_kv_append_paged_e4m3(k.cuda(), v.cuda(), kp, vp, ks, vs, dt, lens, rope,
+                                       new_lens=torch.tensor(prompt, dtype=torch.int32, device="cuda"), kbounds=kb,
+                                       out_lens=after)
+    hist = [(k[b, :prompt[b]], v[b, :prompt[b]]) for b in range(B)]
+    for step in range(steps):
+        kn, vn = (torch.randn(B, 1, Hkv, D, generator=g).to(torch.bfloat16) for _ in range(2))
+        q = (torch.randn(B, Hq, D, generator=g) * 2).to(torch.bfloat16)
+        lens, after = after, torch.empty_like(lens)
+        la.llama_attn_kv_append_paged_e4m3(kn.cuda(), vn.cuda(), kp, vp, ks, vs, dt, lens, rope, kbounds=kb,
+                                           out_lens=after)
+        ids = la.llama_attn_select_blocks(q.cuda(), kb, dt, after, page, 2, 0, 1, q_pos_offset=-1)
+        out = la.llama_attn_decode_paged_sparse_e4m3(q.cuda(), kp, vp, ks, vs, dt, ids, after, q_pos_offset=-1)
+        hist = [(torch.cat([a, kn[b]]), torch.cat([c, vn[b]])) for b, (a, c) in enumerate(hist)]
+        n = [p + step + 1 for p in prompt]
+        assert after.tolist() == n
+        kv = R.codes(kp.cpu()) * ks.cpu().double()[:, :, None, None]
+        vv = R.codes(vp.cpu()) * vs.cpu().double()[:, :, None, None]
+        for b in range(B):  # the cache holds the history, rotated, within one rounding (two where a block grew)
+            row = torch.arange(n[b])
+            pg = table[b, row // page].long()
+            want = (R.rotate(hist[b][0], row[:, None], THETA), hist[b][1].double())
+            for vals, sc, w in ((kv, ks, want[0]), (vv, vs, want[1])):
+                got = vals[pg, :, row % page]
+                one = sc.cpu().double()[pg][..., None]
+                tol = 1.001 * torch.maximum(2.0 ** -4 * w.abs(), 2.0 ** -10 * one) + 2.0 ** -10 * one + 2.0 ** -20
+                assert torch.all((got - w).abs() <= tol)
+        bounds = kb.cpu()
+        assert torch.equal(ids.cpu(), R.select(q, bounds, table, n, page, 2, 0, 1, THETA, -1))
+        ref = R.decode(q, kv, vv, table, n, page, THETA, -1, ids.cpu())
+        check_attention("e4m3", out, None, ref, 8.0, 2 * page)
+
+
+def test_captured_steps_replay_with_new_lengths():
+    """Append, selection and decode in one CUDA graph: lengths and inputs are read at replay."""
+    page, Hq, Hkv, B = 64, 8, 2, 3
+    g = gen(71)
+    table, n_pages = make_table(g, [400, 300, 200], page)
+    dt = table.cuda()
+    rope = la.llama_attn_rope_table_build(table.shape[1] * page, D, THETA)
+    kp, vp = (torch.zeros(n_pages, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kb = torch.zeros(n_pages, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    after, out = torch.empty_like(lens), torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(B, 1, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+    ids = torch.empty(B, Hkv, 3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(la.llama_attn_decode_runs_workspace_size(B, Hq, Hkv), dtype=torch.uint8, device="cuda")
+
+    def step(out):
+        la.llama_attn_kv_append_paged(k, v, kp, vp, dt, lens, rope, kbounds=kb, out_lens=after)
+        la.llama_attn_select_blocks(q, kb, dt, after, page, 3, block_ids=ids, q_pos_offset=-1)
+        la.llama_attn_decode_paged_sparse(q, kp, vp, dt, ids, after, out=out, workspace=ws, q_pos_offset=-1)
+    step(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out)
+    eager = torch.empty_like(out)
+    for i, n in enumerate(([0, 0, 0], [1, 63, 64], [399, 130, 199])):
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, generator=g))
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert after.tolist() == [x + 1 for x in n]
+        step(eager)
+        assert torch.equal(out, eager)
+
+
+def test_two_streams_at_once():
+    """Two decodes that overlap, each with its own workspace, on streams of their own."""
+    cases = []
+    for i, kind in enumerate(("e4m3", "bf16")):
+        s = attention_state(kind, 64, 8, 2, [3000, 1, 2000], 81 + i)
+        d = on_gpu(s)
+        bounds = bounds_of(s).cuda()
+        fn = la.llama_attn_decode_paged_sparse if kind == "bf16" else la.llama_attn_decode_paged_sparse_e4m3
+
+        def one(d=d, bounds=bounds, fn=fn, stream=None):
+            ids = la.llama_attn_select_blocks(d["q"], bounds, d["table"], d["lens"], 64, 9, stream=stream)
+            return fn(d["q"], *d["pools"], *d["scales"], d["table"], ids, d["lens"], stream=stream)
+        cases.append(one)
+    want = [one() for one in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, one in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(one())
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_many_sequences():
+    """More sequences than a CTA has threads, most of them empty or short."""
+    g = gen(91)
+    B, Hq, Hkv, page = 701, 2, 1, 64
+    lens = [int(x) for x in torch.randint(0, 40, (B,), generator=g)]
+    lens[3], lens[700] = 500, 129
+    s = attention_state("e4m3", page, Hq, Hkv, lens, 92)
+    d = on_gpu(s)
+    lse = torch.empty(B, Hq, device="cuda")
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], lse=lse)
+    check_attention("e4m3", out, lse, R.decode(s["q"], s["kv"], s["vv"], s["table"], lens, page, THETA), 7.0, 500)
+    zero = torch.zeros_like(d["lens"])
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], zero, lse=lse)
+    assert not out.any() and torch.isinf(lse).all()
