@@ -516,72 +516,101 @@ def llama_attn_decode_noalloc(q, kcache, vcache, cache_lens, out, rope_theta: fl
 
 
 # ---- paged cache: append, E4M3 decode, block-sparse decode
-def _tensor(name, t, dtypes, shape, dev, contiguous=True):
-    """``t`` is a CUDA tensor on ``dev`` of one of ``dtypes`` and of ``shape`` (None: any extent)."""
-    if (t.device != dev or t.dtype not in dtypes or (contiguous and not t.is_contiguous())
-            or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise ValueError(f"{name}: {'contiguous ' if contiguous else ''}{'/'.join(str(d) for d in dtypes)} tensor of "
-                         f"shape {tuple('*' if n is None else n for n in shape)} on {dev} expected, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+# A decode step makes several of these calls, each a few microseconds of GPU
+# work, so the checks below are written for few interpreter steps.
+def _tensor(name, t, dtype, shape, index):
+    """``t`` is a contiguous tensor of ``dtype`` and ``shape`` on CUDA device ``index``."""
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {index} expected, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
 
 
-def _call(fn, dev, stream, *args):
-    """Calls the library on ``dev`` (tensors may live on another device than the
-    current one) and that device's current stream, or on ``stream``."""
+def _dim(name, t, n):
+    """The shape of ``t``, which has ``n`` dimensions."""
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name}: {n} dimensions expected, got {tuple(shape)}")
+    return shape
+
+
+def _cuda_index(name, t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: CUDA tensor expected")
+    return index
+
+
+def _call(fn, index, stream, *args):
+    """Calls the library on CUDA device ``index`` (which need not be the current
+    one) and that device's current stream, or on ``stream``."""
     import torch
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    _require(s.device == dev, f"stream is on {s.device}, the tensors are on {dev}")
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() == dev.index:
-        st = f(*args, s.cuda_stream)
+    if stream is None:
+        raw = torch.cuda.current_stream(index).cuda_stream
     else:
-        with torch.cuda.device(dev):
-            st = f(*args, s.cuda_stream)
+        _require(stream.device.index == index, f"stream is on {stream.device}, the tensors are on device {index}")
+        raw = stream.cuda_stream
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() == index:
+        st = f(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, raw)
     if st:
         _check(fn, st)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _cuda_device(t, name):
-    _require(t.is_cuda, f"{name}: CUDA tensor expected")
-    return t.device
-
-
-def _append(fn, k, v, pools, scales, block_table, cache_lens, rope_table, new_lens, kbounds, out_lens, dtypes, stream):
+def _pool(kpages, vpages, scales, dtypes, D, index):
+    """Checks a page pool with its scales; (n_pages, Hkv, page_size)."""
     import torch
-    i32 = (torch.int32,)
-    dev = _cuda_device(k, "k")
-    _require(k.dim() == 4, "k must be [B, T, Hkv, 128]")
-    B, T, Hkv, D = k.shape
-    strides = []
+    n_pages, Hkv, page_size, _ = shape = _dim("kpages", kpages, 4)
+    _require(kpages.dtype in dtypes, f"kpages: {kpages.dtype} pages are not supported here")
+    _tensor("kpages", kpages, kpages.dtype, (n_pages, Hkv, page_size, D), index)
+    _tensor("vpages", vpages, kpages.dtype, shape, index)
+    if scales:
+        _tensor("k_scales", scales[0], torch.float32, (n_pages, Hkv), index)
+        _tensor("v_scales", scales[1], torch.float32, (n_pages, Hkv), index)
+    return n_pages, Hkv, page_size
+
+
+def _append(fn, k, v, kpages, vpages, scales, block_table, cache_lens, rope_table, new_lens, kbounds, out_lens, dtypes,
+            stream):
+    import torch
+    i32 = torch.int32
+    index = _cuda_index("k", k)
+    B, T, Hkv, D = shape = _dim("k", k, 4)
     for name, t in (("k", k), ("v", v)):
-        _tensor(name, t, (torch.bfloat16,), (B, T, Hkv, D), dev, contiguous=False)
-        sb, st, sh, sd = t.stride()
-        _require((sd == 1 or D == 1) and (sh == D or Hkv == 1), f"{name}: the heads of a token must be contiguous")
-        strides.append((st if T > 1 else Hkv * D, sb if B > 1 else 0))
-    _require(strides[0] == strides[1], "k and v must have the same strides")
-    kpages, vpages = pools
-    _tensor("kpages", kpages, dtypes, (None, Hkv, None, D), dev)
-    n_pages, page_size = kpages.shape[0], kpages.shape[2]
-    _tensor("vpages", vpages, (kpages.dtype,), (n_pages, Hkv, page_size, D), dev)
-    for name, t in zip(("k_scales", "v_scales"), scales):
-        _tensor(name, t, (torch.float32,), (n_pages, Hkv), dev)
-    _tensor("block_table", block_table, i32, (B, None), dev)
-    _tensor("cache_lens", cache_lens, i32, (B,), dev)
-    _tensor("rope_table", rope_table, (torch.float32,), (None, D // 2, 2), dev)
+        if t.get_device() != index or t.dtype is not torch.bfloat16 or t.shape != shape:
+            raise ValueError(f"{name}: bfloat16 tensor of shape {tuple(shape)} on CUDA device {index} expected, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    sb, st, sh, sd = k.stride()
+    if k.is_contiguous() and v.is_contiguous():
+        st, sb = Hkv * D, T * Hkv * D
+    else:
+        vb, vt, vh, vd = v.stride()
+        _require((sd == vd == 1 or D == 1) and (sh == vh == D or Hkv == 1),
+                 "k and v: the heads of a token must be contiguous")
+        _require((st == vt or T == 1) and (sb == vb or B == 1), "k and v must have the same strides")
+        st, sb = st if T > 1 else Hkv * D, sb if B > 1 else 0
+    n_pages, pool_heads, page_size = _pool(kpages, vpages, scales, dtypes, D, index)
+    _require(pool_heads == Hkv, f"kpages: {Hkv} KV heads expected, got {pool_heads}")
+    max_blocks = _dim("block_table", block_table, 2)[1]
+    _tensor("block_table", block_table, i32, (B, max_blocks), index)
+    _tensor("cache_lens", cache_lens, i32, (B,), index)
+    rows = _dim("rope_table", rope_table, 3)[0]
+    _tensor("rope_table", rope_table, torch.float32, (rows, D // 2, 2), index)
+    new = out = bounds = None
     if new_lens is not None:
-        _tensor("new_lens", new_lens, i32, (B,), dev)
+        _tensor("new_lens", new_lens, i32, (B,), index)
+        new = new_lens.data_ptr()
     if out_lens is not None:
-        _tensor("out_lens", out_lens, i32, (B,), dev)
+        _tensor("out_lens", out_lens, i32, (B,), index)
+        out = out_lens.data_ptr()
     if kbounds is not None:
-        _tensor("kbounds", kbounds, (torch.bfloat16,), (n_pages, Hkv, 2, D), dev)
-    _call(fn, dev, stream, k.data_ptr(), v.data_ptr(), *strides[0], kpages.data_ptr(), vpages.data_ptr(),
-          *(t.data_ptr() for t in scales), _addr(kbounds), block_table.data_ptr(), cache_lens.data_ptr(),
-          _addr(new_lens), _addr(out_lens), B, T, Hkv, D, page_size, block_table.shape[1], n_pages,
-          rope_table.data_ptr(), rope_table.shape[0])
+        _tensor("kbounds", kbounds, torch.bfloat16, (n_pages, Hkv, 2, D), index)
+        bounds = kbounds.data_ptr()
+    _call(fn, index, stream, k.data_ptr(), v.data_ptr(), st, sb, kpages.data_ptr(), vpages.data_ptr(),
+          *[t.data_ptr() for t in scales], bounds, block_table.data_ptr(), cache_lens.data_ptr(), new, out, B, T, Hkv,
+          D, page_size, max_blocks, n_pages, rope_table.data_ptr(), rows)
     return out_lens
 
 
@@ -595,7 +624,7 @@ def llama_attn_kv_append_paged(k, v, kpages, vpages, block_table, cache_lens, ro
     kbounds bf16 [n_pages,Hkv,2,128]: per block least and greatest key, kept for
     llama_attn_select_blocks. out_lens int32 [B] gets the new lengths. Returns out_lens."""
     import torch
-    return _append("llama_attn_kv_append_paged", k, v, (kpages, vpages), (), block_table, cache_lens, rope_table,
+    return _append("llama_attn_kv_append_paged", k, v, kpages, vpages, (), block_table, cache_lens, rope_table,
                    new_lens, kbounds, out_lens, (torch.bfloat16,), stream)
 
 
@@ -604,7 +633,7 @@ def llama_attn_kv_append_paged_e4m3(k, v, kpages, vpages, k_scales, v_scales, bl
     """llama_attn_kv_append_paged into E4M3 pages (uint8 or float8_e4m3fn) with
     one float32 scale per page and KV head, k_scales and v_scales [n_pages,Hkv]."""
     import torch
-    return _append("llama_attn_kv_append_paged_e4m3", k, v, (kpages, vpages), (k_scales, v_scales), block_table,
+    return _append("llama_attn_kv_append_paged_e4m3", k, v, kpages, vpages, (k_scales, v_scales), block_table,
                    cache_lens, rope_table, new_lens, kbounds, out_lens, (torch.uint8, torch.float8_e4m3fn), stream)
 
 
@@ -613,38 +642,38 @@ def llama_attn_decode_runs_workspace_size(B: int, Hq: int, Hkv: int, D: int = 12
     return int(lib().llama_attn_decode_runs_workspace_size(int(B), int(Hq), int(Hkv), int(D)))
 
 
-def _decode_runs(fn, q, pools, scales, block_table, block_ids, cache_lens, out, lse, workspace, q_pos_offset,
+def _decode_runs(fn, q, kpages, vpages, scales, block_table, block_ids, cache_lens, out, lse, workspace, q_pos_offset,
                  rope_theta, dtypes, stream):
     import torch
-    i32 = (torch.int32,)
-    dev = _cuda_device(q, "q")
-    _tensor("q", q, (torch.bfloat16,), (None, None, None), dev)
-    B, Hq, D = q.shape
-    kpages, vpages = pools
-    _tensor("kpages", kpages, dtypes, (None, None, None, D), dev)
-    n_pages, Hkv, page_size, _ = kpages.shape
-    _tensor("vpages", vpages, (kpages.dtype,), (n_pages, Hkv, page_size, D), dev)
-    for name, t in zip(("k_scales", "v_scales"), scales):
-        _tensor(name, t, (torch.float32,), (n_pages, Hkv), dev)
-    _tensor("block_table", block_table, i32, (B, None), dev)
-    _tensor("cache_lens", cache_lens, i32, (B,), dev)
+    i32 = torch.int32
+    index = _cuda_index("q", q)
+    B, Hq, D = shape = _dim("q", q, 3)
+    _tensor("q", q, torch.bfloat16, shape, index)
+    n_pages, Hkv, page_size = _pool(kpages, vpages, scales, dtypes, D, index)
+    max_blocks = _dim("block_table", block_table, 2)[1]
+    _tensor("block_table", block_table, i32, (B, max_blocks), index)
+    _tensor("cache_lens", cache_lens, i32, (B,), index)
     if out is None:
         out = torch.empty_like(q)
-    _tensor("out", out, (torch.bfloat16,), (B, Hq, D), dev)
+    _tensor("out", out, torch.bfloat16, shape, index)
     if lse is not None:
-        _tensor("lse", lse, (torch.float32,), (B, Hq), dev)
+        _tensor("lse", lse, torch.float32, (B, Hq), index)
+        lse = lse.data_ptr()
     if workspace is None:
         workspace = torch.empty(max(1, llama_attn_decode_runs_workspace_size(B, Hq, Hkv, D)), dtype=torch.uint8,
-                                device=dev)
-    _require(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous tensor on {dev} expected")
-    ids, n_sel = (), ()
-    if block_ids is not None:
-        _tensor("block_ids", block_ids, i32, (B, Hkv, None), dev)
-        ids, n_sel = (block_ids.data_ptr(),), (block_ids.shape[2],)
-    _call(fn, dev, stream, q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), *(t.data_ptr() for t in scales),
-          block_table.data_ptr(), *ids, cache_lens.data_ptr(), out.data_ptr(), _addr(lse), B, Hq, Hkv, D, page_size,
-          block_table.shape[1], n_pages, *n_sel, q_pos_offset, rope_theta, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+                                device=q.device)
+    _require(workspace.get_device() == index and workspace.is_contiguous(),
+             f"workspace: contiguous tensor on CUDA device {index} expected")
+    pools = (q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), *[t.data_ptr() for t in scales],
+             block_table.data_ptr())
+    sizes = (out.data_ptr(), lse, B, Hq, Hkv, D, page_size, max_blocks, n_pages)
+    tail = (q_pos_offset, rope_theta, workspace.data_ptr(), workspace.nbytes)
+    if block_ids is None:
+        _call(fn, index, stream, *pools, cache_lens.data_ptr(), *sizes, *tail)
+    else:
+        n_sel = _dim("block_ids", block_ids, 3)[2]
+        _tensor("block_ids", block_ids, i32, (B, Hkv, n_sel), index)
+        _call(fn, index, stream, *pools, block_ids.data_ptr(), cache_lens.data_ptr(), *sizes, n_sel, *tail)
     return out
 
 
@@ -656,7 +685,7 @@ def llama_attn_decode_paged_e4m3(q, kpages, vpages, k_scales, v_scales, block_ta
     its own key has been appended. lse float32 [B,Hq] (optional) gets the
     log-sum-exp. Returns out [B,Hq,128]."""
     import torch
-    return _decode_runs("llama_attn_decode_paged_e4m3", q, (kpages, vpages), (k_scales, v_scales), block_table, None,
+    return _decode_runs("llama_attn_decode_paged_e4m3", q, kpages, vpages, (k_scales, v_scales), block_table, None,
                         cache_lens, out, lse, workspace, q_pos_offset, rope_theta,
                         (torch.uint8, torch.float8_e4m3fn), stream)
 
@@ -669,20 +698,21 @@ def llama_attn_select_blocks(q, kbounds, block_table, cache_lens, page_size: int
     the group's products with a key of the block (kbounds, as the append keeps
     them). Returns block_ids int32 [B,Hkv,n_sel], ascending, -1 behind the last."""
     import torch
-    i32 = (torch.int32,)
-    dev = _cuda_device(q, "q")
-    _tensor("q", q, (torch.bfloat16,), (None, None, None), dev)
-    B, Hq, D = q.shape
-    _tensor("kbounds", kbounds, (torch.bfloat16,), (None, None, 2, D), dev)
-    n_pages, Hkv = kbounds.shape[:2]
-    _tensor("block_table", block_table, i32, (B, None), dev)
-    _tensor("cache_lens", cache_lens, i32, (B,), dev)
+    i32 = torch.int32
+    index = _cuda_index("q", q)
+    B, Hq, D = shape = _dim("q", q, 3)
+    _tensor("q", q, torch.bfloat16, shape, index)
+    n_pages, Hkv, _, _ = _dim("kbounds", kbounds, 4)
+    _tensor("kbounds", kbounds, torch.bfloat16, (n_pages, Hkv, 2, D), index)
+    max_blocks = _dim("block_table", block_table, 2)[1]
+    _tensor("block_table", block_table, i32, (B, max_blocks), index)
+    _tensor("cache_lens", cache_lens, i32, (B,), index)
     if block_ids is None:
-        block_ids = torch.empty(B, Hkv, n_sel, dtype=torch.int32, device=dev)
-    _tensor("block_ids", block_ids, i32, (B, Hkv, n_sel), dev)
-    _call("llama_attn_select_blocks", dev, stream, q.data_ptr(), kbounds.data_ptr(), block_table.data_ptr(),
-          cache_lens.data_ptr(), block_ids.data_ptr(), B, Hq, Hkv, D, page_size, block_table.shape[1], n_pages, n_sel,
-          n_first, n_last, q_pos_offset, rope_theta)
+        block_ids = torch.empty(B, Hkv, n_sel, dtype=i32, device=q.device)
+    _tensor("block_ids", block_ids, i32, (B, Hkv, n_sel), index)
+    _call("llama_attn_select_blocks", index, stream, q.data_ptr(), kbounds.data_ptr(), block_table.data_ptr(),
+          cache_lens.data_ptr(), block_ids.data_ptr(), B, Hq, Hkv, D, page_size, max_blocks, n_pages, n_sel, n_first,
+          n_last, q_pos_offset, rope_theta)
     return block_ids
 
 
@@ -693,7 +723,7 @@ def llama_attn_decode_paged_sparse(q, kpages, vpages, block_table, block_ids, ca
     llama_attn_select_blocks gives them). Other arguments as for
     llama_attn_decode_paged_e4m3. Returns out [B,Hq,128]."""
     import torch
-    return _decode_runs("llama_attn_decode_paged_sparse", q, (kpages, vpages), (), block_table, block_ids, cache_lens,
+    return _decode_runs("llama_attn_decode_paged_sparse", q, kpages, vpages, (), block_table, block_ids, cache_lens,
                         out, lse, workspace, q_pos_offset, rope_theta, (torch.bfloat16,), stream)
 
 
@@ -702,7 +732,7 @@ def llama_attn_decode_paged_sparse_e4m3(q, kpages, vpages, k_scales, v_scales, b
                                         rope_theta: float = 500000.0, stream=None):
     """llama_attn_decode_paged_sparse over an E4M3 page pool with its scales."""
     import torch
-    return _decode_runs("llama_attn_decode_paged_sparse_e4m3", q, (kpages, vpages), (k_scales, v_scales), block_table,
+    return _decode_runs("llama_attn_decode_paged_sparse_e4m3", q, kpages, vpages, (k_scales, v_scales), block_table,
                         block_ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta,
                         (torch.uint8, torch.float8_e4m3fn), stream)
 

@@ -266,6 +266,7 @@ int device_setup(int dev, int* n_sm) {
     attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, true>), la::dpg::Tile<true>::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, false>), la::dpg::Tile<false>::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, true>), la::dpg::Tile<false>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::pap::kv_append_paged_kernel<true, 256, 8>), 256 * 8 * 32);
     attr(reinterpret_cast<const void*>(la::sel::select_blocks_kernel), la::sel::MAX_BLOCKS * 8);
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) ds.n_sm = n;
@@ -979,17 +980,22 @@ int kv_append_paged(const AppendArgs& a, cudaStream_t stream) {
   // blocks that T rows can touch, wherever in a block they begin
   int64_t slots = (static_cast<int64_t>(a.T) + a.page_size - 2) / a.page_size + 1;
   if (slots > a.max_blocks) slots = a.max_blocks;
-  const dim3 grid(static_cast<unsigned>(slots), a.Hkv, a.B);
+  if (slots > 65535) return LLAMA_ATTN_ERR_UNSUPPORTED;
+  const dim3 grid(2 * a.Hkv, static_cast<unsigned>(slots), a.B);
+  int dev;
+  if ((st = current_device(&dev))) return st;
+  if ((st = device_setup(dev, nullptr))) return st;
   std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
   prof_count(1);
   const int pair = prof_before(stream);
   const int rows = a.T < a.page_size ? a.T : a.page_size;  // a CTA's rows at most
+  auto smem = [](int threads, int rows_per_thread) { return kE4M3 ? threads * rows_per_thread * 32 : 0; };
   if (rows <= 16)
-    la::pap::kv_append_paged_kernel<kE4M3, 64><<<grid, 64, 0, stream>>>(p);
+    la::pap::kv_append_paged_kernel<kE4M3, 128, 2><<<grid, 128, smem(128, 2), stream>>>(p);
   else if (rows <= 64)
-    la::pap::kv_append_paged_kernel<kE4M3, 256><<<grid, 256, 0, stream>>>(p);
+    la::pap::kv_append_paged_kernel<kE4M3, 128, 8><<<grid, 128, smem(128, 8), stream>>>(p);
   else
-    la::pap::kv_append_paged_kernel<kE4M3, 512><<<grid, 512, 0, stream>>>(p);
+    la::pap::kv_append_paged_kernel<kE4M3, 256, 8><<<grid, 256, smem(256, 8), stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   prof_after(pair, stream);
   return cuda_status(e);

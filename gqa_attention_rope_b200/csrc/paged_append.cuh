@@ -16,11 +16,13 @@
 // Key bounds: per block, head and channel the least and the greatest rotated
 // key, in bf16 (rounding is monotone, so it commutes with min and max).
 //
-// Work split: one CTA owns one (sequence, logical block, KV head), so the
-// block's amax, scale and bounds need no atomics. Half of its threads take K,
-// the other half V, 16 threads per row with 16 bytes each. The bound is the
-// memory traffic: 512 bytes read and 256 (E4M3) or 512 (bf16) written per token
-// and head; up to 8 rows per thread wait in registers for the block's scale.
+// Work split: one CTA owns K or V of one (sequence, logical block, KV head),
+// so the block's amax, scale and bounds need no atomics. 16 threads take a row,
+// 16 bytes each, and a thread up to 8 rows. The bound is the memory traffic
+// (512 bytes read and 256 (E4M3) or 512 (bf16) written per token and head) and,
+// for E4M3 keys, issue and latency: all loads of a thread are issued before
+// the first is used, and before the page is looked up (rows past the end read
+// the last row again instead of branching).
 #pragma once
 
 #include "ptx.cuh"
@@ -28,7 +30,6 @@
 namespace la {
 namespace pap {
 
-constexpr int kMaxRowsPerThread = 8;
 constexpr int kMinExp = -100, kMaxExp = 119;  // exponents of the block scales
 
 struct Params {
@@ -64,6 +65,15 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
   return __half22float2(v);
 }
 
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, u;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 u, %4, %3;\n\tmov.b32 %0, {l, u};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
 // Every code of the 4 in `w` multiplied by r and rounded again.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
   const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(w & 0xFFFFu));
@@ -71,21 +81,25 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
   return e4m3x2(a.x * r, a.y * r) | (e4m3x2(b.x * r, b.y * r) << 16);
 }
 
-// Eight values of one row (this thread's channels) in float32.
-__device__ __forceinline__ void load_row(const uint16_t* src, float (&x)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+__device__ __forceinline__ uint4 load_row(const uint16_t* src) {
+  uint4 u;  // read once: not kept in L1
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(src));
+  return u;
+}
+__device__ __forceinline__ void unpack_row(const uint4& u, float (&x)[8]) {
   const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
   x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
 }
-// The four pairs of this thread turned by the table row (no contraction into
-// FMA: the rounding is the one stated above on every path).
-__device__ __forceinline__ void rotate_row(const float4* tab_row, float (&x)[8]) {
+// The four pairs of this thread turned by its part of the table row (no
+// contraction into FMA: the rounding is the one stated above on every path).
+__device__ __forceinline__ void rotate_row(const float4 (&cs)[2], float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 cs = __ldg(tab_row + i);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float c = j ? cs.z : cs.x, s = j ? cs.w : cs.y;
+      const float c = j ? cs[i].z : cs[i].x, s = j ? cs[i].w : cs[i].y;
       const float a = x[4 * i + 2 * j], b = x[4 * i + 2 * j + 1];
       x[4 * i + 2 * j] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
       x[4 * i + 2 * j + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
@@ -93,148 +107,296 @@ __device__ __forceinline__ void rotate_row(const float4* tab_row, float (&x)[8])
   }
 }
 
-// grid (block slots, Hkv, B), kThreads threads. A page of more than
-// kThreads / 32 * 8 new rows is read twice (the second time from L2).
-template <bool kE4M3, int kThreads>
-__global__ void __launch_bounds__(kThreads) kv_append_paged_kernel(const Params p) {
-  constexpr int kWarps = kThreads / 32;
-  constexpr int kRowsPerPass = kThreads / 32;  // per half: (kThreads / 2) / 16
-  constexpr int kTile = kRowsPerPass * kMaxRowsPerThread;
-  __shared__ float s_amax[kWarps];
-  __shared__ float s_bound[kWarps / 2][2][128];
+// 16 bytes from global to this thread's own place in shared memory, asynchronously.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int64_t len = p.lens[b];
-  const int64_t n_new = p.new_lens ? p.new_lens[b] : p.T;
-  const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.page_size;
-  const bool ok = len >= 0 && n_new >= 0 && n_new <= p.T && len + n_new <= cap;
-  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
-    if (!ok) raise_error(LLAMA_ATTN_DEVERR_CACHE_LEN);
-    if (p.out_lens) p.out_lens[b] = static_cast<int32_t>(ok ? len + n_new : len);
-  }
-  if (!ok) return;
-  const int64_t blk = len / p.page_size + blockIdx.x;
-  const int64_t first = blk * p.page_size;                   // the block's first position
-  const int64_t r0 = len > first ? len : first;
-  const int64_t r1 = min(len + n_new, first + p.page_size);
-  if (r0 >= r1) return;
-  const int page = p.block_table[static_cast<int64_t>(b) * p.max_blocks + blk];
+// What one CTA does: rows [r0, r0 + n) of sequence b, all in logical block
+// blk, which holds `was` rows already; K or V of KV head h.
+struct Job {
+  int b, h, blk, len, r0, n, was;
+};
+
+// The page of the job's block times Hkv plus its head, or -1 with the error raised.
+__device__ __forceinline__ int64_t page_head(const Params& p, const Job& j) {
+  const int page = p.block_table[static_cast<int64_t>(j.b) * p.max_blocks + j.blk];
   if (page < 0 || page >= p.n_pages) {
     if (threadIdx.x == 0) raise_error(LLAMA_ATTN_DEVERR_BLOCK_TABLE);
+    return -1;
+  }
+  return static_cast<int64_t>(page) * p.Hkv + j.h;
+}
+__device__ __forceinline__ const uint16_t* first_row(const Params& p, const Job& j, const uint16_t* x) {
+  return x + j.b * p.batch_stride + (j.r0 - j.len) * p.row_stride + j.h * 128 + (threadIdx.x & 15) * 8;
+}
+// Row of a thread's i-th slot; past the end the last row again (it changes no range and is not stored).
+template <int kRowsPerPass>
+__device__ __forceinline__ int slot_row(int t0, int i, int n) {
+  return min(t0 + static_cast<int>(threadIdx.x >> 4) + i * kRowsPerPass, n - 1);
+}
+
+// The block's new scale from this thread's greatest magnitude; codes that the
+// block holds already follow it. All threads of the CTA; s_amax: one per warp.
+template <int kThreads>
+__device__ __forceinline__ float settle_scale(const Job& j, float amax, float old_scale, float* scale_at, uint8_t* codes,
+                                              float* s_amax) {
+  const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));  // magnitudes order like their bits
+  if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = __uint_as_float(a);
+  __syncthreads();
+  float m = s_amax[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_amax[w]);
+  float scale = exp2i(scale_exp(m));
+  if (j.was > 0) scale = fmaxf(scale, old_scale);
+  if (j.was > 0 && scale != old_scale) {
+    const float r = old_scale / scale;
+    uint4* at = reinterpret_cast<uint4*>(codes);
+    for (int i = threadIdx.x; i < j.was * 8; i += kThreads) {
+      const uint4 c = at[i];
+      at[i] = make_uint4(rescale4(c.x, r), rescale4(c.y, r), rescale4(c.z, r), rescale4(c.w, r));
+    }
+  }
+  if (threadIdx.x == 0) *scale_at = scale;
+  return scale;
+}
+// A warp's channel-wise ranges into shared memory, and (after a barrier) the
+// CTA's into the block's bounds, which they widen where the block had rows.
+__device__ __forceinline__ void gather_bounds(float (&lo)[8], float (&hi)[8], float (*s_bound)[2][128]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    lo[c] = fminf(lo[c], __shfl_xor_sync(0xffffffffu, lo[c], 16));
+    hi[c] = fmaxf(hi[c], __shfl_xor_sync(0xffffffffu, hi[c], 16));
+  }
+  const bool upper = lane >= 16;  // lanes 0-15 write the minima, 16-31 the maxima
+  float4* at = reinterpret_cast<float4*>(&s_bound[threadIdx.x >> 5][upper][(lane & 15) * 8]);
+  at[0] = upper ? make_float4(hi[0], hi[1], hi[2], hi[3]) : make_float4(lo[0], lo[1], lo[2], lo[3]);
+  at[1] = upper ? make_float4(hi[4], hi[5], hi[6], hi[7]) : make_float4(lo[4], lo[5], lo[6], lo[7]);
+}
+template <int kThreads>
+__device__ __forceinline__ void store_bounds(uint16_t* bounds, bool widen, float (*s_bound)[2][128]) {
+  for (int i = threadIdx.x; i < 256; i += kThreads) {  // 128 minima, then 128 maxima
+    const int m = i >> 7, c = i & 127;
+    const float sign = m ? -1.f : 1.f;  // max x = -min(-x)
+    float x = sign * s_bound[0][m][c];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) x = fminf(x, sign * s_bound[w][m][c]);
+    if (widen) x = fminf(x, sign * __uint_as_float(static_cast<uint32_t>(bounds[i]) << 16));
+    const __nv_bfloat16 y = __float2bfloat16_rn(sign * x);
+    bounds[i] = *reinterpret_cast<const uint16_t*>(&y);
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t* dst, float (&x)[8], uint64_t inv) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), inv), x[j], x[j + 1]);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+}
+
+// Values: copied, or coded once the scale is known from rows kept in registers.
+template <bool kE4M3, int kThreads, int kRows>
+__device__ __forceinline__ void append_values(const Params& p, const Job& j, float* s_amax) {
+  constexpr int kRowsPerPass = kThreads / 16;
+  constexpr int kHeld = kRowsPerPass * kRows;
+  const int n = j.n, row0 = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
+  const uint16_t* src = first_row(p, j, p.v);
+  uint4 raw[kRows];
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) raw[i] = load_row(src + slot_row<kRowsPerPass>(t0, i, n) * p.row_stride);
+  };
+  fetch(0);  // on their way before the page is looked up
+  const int64_t ph = page_head(p, j);
+  if (ph < 0) return;
+  const int64_t dst0 = (ph * p.page_size + j.was) * 128 + ch;
+  if constexpr (!kE4M3) {
+    for (int t0 = 0; t0 < n; t0 += kHeld) {
+      if (t0 > 0) fetch(t0);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = t0 + row0 + i * kRowsPerPass;
+        if (r < n) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.vpages) + dst0 + r * 128) = raw[i];
+      }
+    }
+  } else {
+    const float old_scale = j.was > 0 ? p.vscales[ph] : 0.f;
+    uint32_t m = 0u;  // greatest magnitudes of even and odd channels, as bf16 bits
+    for (int t0 = 0; t0 < n; t0 += kHeld) {
+      if (t0 > 0) fetch(t0);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu),
+                                 __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu)));
+    }
+    const float amax = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    uint8_t* pages = static_cast<uint8_t*>(p.vpages);
+    const float scale = settle_scale<kThreads>(j, amax, old_scale, p.vscales + ph, pages + ph * p.page_size * 128, s_amax);
+    const uint64_t inv = f2_pack(1.f / scale, 1.f / scale);
+    for (int t0 = 0; t0 < n; t0 += kHeld) {
+      if (n > kHeld) fetch(t0);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        float x[8];
+        unpack_row(raw[i], x);
+        const int r = t0 + row0 + i * kRowsPerPass;
+        if (r < n) store_codes(pages + dst0 + r * 128, x, inv);
+      }
+    }
+  }
+}
+
+// Keys. Table rows come along in registers, half of a thread's rows at a time.
+// bf16: rotated and stored. E4M3: all rows are first copied into shared memory,
+// each thread its own 16 bytes of a row; the rotated row takes the copy's place
+// and waits there for the scale.
+template <bool kE4M3, int kThreads, int kRows>
+__device__ __forceinline__ void append_keys(const Params& p, const Job& j, float* s_amax, float (*s_bound)[2][128]) {
+  constexpr int kRowsPerPass = kThreads / 16;
+  constexpr int kStep = kRows / 2;
+  constexpr int kHeld = kRowsPerPass * kRows;
+  extern __shared__ float4 s_keep[];  // [row slot][half][thread]
+  const int n = j.n, row0 = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
+  const uint16_t* src = first_row(p, j, p.k);
+  const float4* tab = p.tab + static_cast<int64_t>(j.r0) * 32 + ch / 4;
+  auto row = [&](int t0, int i) { return slot_row<kRowsPerPass>(t0, i, n); };
+  auto kept = [&](int i) { return s_keep + 2 * kThreads * i + threadIdx.x; };
+
+  uint4 raw[kStep];
+  auto fetch = [&](int t0, int i0) {  // E4M3: the tile; bf16: a step of it from slot i0
+#pragma unroll
+    for (int i = 0; i < (kE4M3 ? kRows : kStep); ++i) {
+      if constexpr (kE4M3)
+        copy_async16(kept(i), src + row(t0, i) * p.row_stride);
+      else
+        raw[i] = load_row(src + row(t0, i0 + i) * p.row_stride);
+    }
+  };
+  fetch(0, 0);  // on their way before the page is looked up
+  const int64_t ph = page_head(p, j);
+  if (ph < 0) {
+    if constexpr (kE4M3) copy_async_wait();
     return;
   }
-  const int64_t ph = static_cast<int64_t>(page) * p.Hkv + h;
-  const int was = static_cast<int>(r0 - first);              // rows the block already holds
-  const int n = static_cast<int>(r1 - r0);
-
-  const bool is_v = threadIdx.x >= kThreads / 2;
-  const int tid = threadIdx.x - (is_v ? kThreads / 2 : 0);
-  const int row0 = tid >> 4, ch = (tid & 15) * 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint16_t* src = (is_v ? p.v : p.k) + b * p.batch_stride + (r0 - len) * p.row_stride + h * 128 + ch;
-  const float4* tab = p.tab + r0 * 32 + ch / 4;
-
-  auto fetch = [&](int r, float (&x)[8]) {
-    load_row(src + r * p.row_stride, x);
-    if (!is_v) rotate_row(tab + static_cast<int64_t>(r) * 32, x);
-  };
-  auto store_bf16 = [&](int r, const float (&x)[8]) {
-    uint16_t* dst = static_cast<uint16_t*>(is_v ? p.vpages : p.kpages) + (ph * p.page_size + was + r) * 128 + ch;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-  };
-  auto store_e4m3 = [&](int r, const float (&x)[8], float inv) {
-    uint8_t* dst = static_cast<uint8_t*>(is_v ? p.vpages : p.kpages) + (ph * p.page_size + was + r) * 128 + ch;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16),
-                   e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16));
-  };
-
-  float keep[kMaxRowsPerThread][8];
-  float lo[8], hi[8], amax = 0.f;
+  const int64_t dst0 = (ph * p.page_size + j.was) * 128 + ch;
+  const float old_scale = kE4M3 && j.was > 0 ? p.kscales[ph] : 0.f;
+  const bool ranges = kE4M3 || p.kbounds;
+  float lo[8], hi[8];  // of the thread's channels
 #pragma unroll
-  for (int i = 0; i < 8; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
-  for (int t0 = 0; t0 < n; t0 += kTile) {
+  for (int c = 0; c < 8; ++c) lo[c] = INFINITY, hi[c] = -INFINITY;
+  auto rotate_tile = [&](int t0) {
 #pragma unroll
-    for (int i = 0; i < kMaxRowsPerThread; ++i) {
-      const int r = t0 + row0 + i * kRowsPerPass;
-      if (r < n) fetch(r, keep[i]);
-    }
+    for (int half = 0; half < 2; ++half) {
+      if constexpr (!kE4M3) {
+        if (t0 + half > 0) fetch(t0, half * kStep);
+      }
+      float4 cs[kStep][2];
 #pragma unroll
-    for (int i = 0; i < kMaxRowsPerThread; ++i) {
-      const int r = t0 + row0 + i * kRowsPerPass;
-      if (r < n) {
+      for (int i = 0; i < kStep; ++i) {
+        const float4* c = tab + row(t0, half * kStep + i) * 32;
+        cs[i][0] = __ldg(c);
+        cs[i][1] = __ldg(c + 1);
+      }
+      if constexpr (kE4M3) {
+        if (half == 0) copy_async_wait();
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          lo[j] = fminf(lo[j], keep[i][j]);
-          hi[j] = fmaxf(hi[j], keep[i][j]);
+      for (int i = 0; i < kStep; ++i) {
+        const int s = half * kStep + i;
+        float x[8];
+        if constexpr (kE4M3)
+          unpack_row(*reinterpret_cast<const uint4*>(kept(s)), x);
+        else
+          unpack_row(raw[i], x);
+        rotate_row(cs[i], x);
+        if (ranges) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) lo[c] = fminf(lo[c], x[c]), hi[c] = fmaxf(hi[c], x[c]);
         }
-        if constexpr (!kE4M3) store_bf16(r, keep[i]);
+        if constexpr (kE4M3) {
+          kept(s)[0] = make_float4(x[0], x[1], x[2], x[3]);
+          kept(s)[kThreads] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+          const int r = t0 + row0 + s * kRowsPerPass;
+          if (r < n)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kpages) + dst0 + r * 128) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                           pack_bf16x2(x[6], x[7]));
+        }
       }
     }
+  };
+  for (int t0 = 0; t0 < n; t0 += kHeld) {
+    if (kE4M3 && t0 > 0) fetch(t0, 0);
+    rotate_tile(t0);
   }
+  if (!ranges) return;
+  float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(-lo[j], hi[j]));  // no row: -inf, -inf
-
-  float old_scale = 0.f;
-  float* scales = nullptr;
+  for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fmaxf(-lo[c], hi[c]));
+  if (p.kbounds) gather_bounds(lo, hi, s_bound);
+  float scale = 1.f;
+  uint8_t* pages = static_cast<uint8_t*>(p.kpages);
+  if constexpr (kE4M3)
+    scale = settle_scale<kThreads>(j, amax, old_scale, p.kscales + ph, pages + ph * p.page_size * 128, s_amax);
+  else
+    __syncthreads();
+  if (p.kbounds) store_bounds<kThreads>(p.kbounds + ph * 256, j.was > 0, s_bound);
   if constexpr (kE4M3) {
-    scales = (is_v ? p.vscales : p.kscales) + ph;
-    if (was > 0) old_scale = *scales;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (lane == 0) s_amax[warp] = amax;
-  }
-  if (p.kbounds && !is_v) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], 16));
-      hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], 16));
-      if (lane < 16) s_bound[warp][0][ch + j] = lo[j], s_bound[warp][1][ch + j] = hi[j];
-    }
-  }
-  __syncthreads();
-  if (p.kbounds) {
-    for (int i = threadIdx.x; i < 256; i += kThreads) {  // 128 minima, then 128 maxima
-      const int m = i >> 7, c = i & 127;
-      float x = s_bound[0][m][c];
-      for (int w = 1; w < kWarps / 2; ++w) x = m ? fmaxf(x, s_bound[w][m][c]) : fminf(x, s_bound[w][m][c]);
-      uint16_t* dst = p.kbounds + ph * 256 + i;
-      if (was > 0) {
-        const float old = __uint_as_float(static_cast<uint32_t>(*dst) << 16);
-        x = m ? fmaxf(x, old) : fminf(x, old);
+    const uint64_t inv = f2_pack(1.f / scale, 1.f / scale);
+    for (int t0 = 0; t0 < n; t0 += kHeld) {
+      if (n > kHeld) {  // a page of more rows than are held: once more, from L2
+        fetch(t0, 0);
+        rotate_tile(t0);
       }
-      const __nv_bfloat16 y = __float2bfloat16_rn(x);
-      *dst = *reinterpret_cast<const uint16_t*>(&y);
-    }
-  }
-  if constexpr (kE4M3) {
-    float a = 0.f;
-    for (int w = 0; w < kWarps / 2; ++w) a = fmaxf(a, s_amax[(is_v ? kWarps / 2 : 0) + w]);
-    float scale = exp2i(scale_exp(a));
-    if (was > 0) scale = fmaxf(scale, old_scale);
-    if (was > 0 && scale != old_scale) {  // the rows already there follow the block's scale
-      const float r = old_scale / scale;
-      uint4* codes = reinterpret_cast<uint4*>(static_cast<uint8_t*>(is_v ? p.vpages : p.kpages) +
-                                              ph * p.page_size * 128);
-      for (int i = tid; i < was * 8; i += kThreads / 2) {
-        const uint4 c = codes[i];
-        codes[i] = make_uint4(rescale4(c.x, r), rescale4(c.y, r), rescale4(c.z, r), rescale4(c.w, r));
-      }
-    }
-    if (tid == 0) *scales = scale;
-    const float inv = 1.f / scale;
-    for (int t0 = 0; t0 < n; t0 += kTile) {
 #pragma unroll
-      for (int i = 0; i < kMaxRowsPerThread; ++i) {
+      for (int i = 0; i < kRows; ++i) {
+        const float4 u = kept(i)[0], w = kept(i)[kThreads];
+        float x[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
         const int r = t0 + row0 + i * kRowsPerPass;
-        if (r < n) {
-          if (n > kTile) fetch(r, keep[i]);
-          store_e4m3(r, keep[i], inv);
-        }
+        if (r < n) store_codes(pages + dst0 + r * 128, x, inv);
       }
     }
   }
+}
+
+// Rows that slot `slot` (the slot-th block that sequence b's new rows touch)
+// and KV head h get; n <= 0: none. `first_cta`: this CTA reports for the sequence.
+__device__ __forceinline__ Job job_of(const Params& p, int b, int slot, int h, bool first_cta) {
+  Job j;
+  j.b = b;
+  j.h = h;
+  j.len = p.lens[b];
+  j.n = 0;
+  j.blk = j.r0 = j.was = 0;
+  const int n_new = p.new_lens ? p.new_lens[b] : p.T;
+  const int cap = p.max_blocks * p.page_size;  // below 2^31
+  const bool ok = j.len >= 0 && n_new >= 0 && n_new <= p.T && j.len <= cap && n_new <= cap - j.len;
+  if (first_cta && threadIdx.x == 0) {
+    if (!ok) raise_error(LLAMA_ATTN_DEVERR_CACHE_LEN);
+    if (p.out_lens) p.out_lens[b] = ok ? j.len + n_new : j.len;
+  }
+  if (!ok) return j;
+  j.blk = j.len / p.page_size + slot;
+  if (j.blk >= p.max_blocks) return j;
+  const int first = j.blk * p.page_size;  // the block's first position
+  j.r0 = max(j.len, first);
+  j.n = min(j.len + n_new - j.r0, first + p.page_size - j.r0);
+  j.was = j.r0 - first;
+  return j;
+}
+
+// One block and K or V of one head per CTA: grid (2 * Hkv, block slots, B).
+template <bool kE4M3, int kThreads, int kRows>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 6) kv_append_paged_kernel(const Params p) {
+  __shared__ float s_amax[kThreads / 32];
+  __shared__ __align__(16) float s_bound[kThreads / 32][2][128];
+  const Job j = job_of(p, blockIdx.z, blockIdx.y, blockIdx.x >> 1, blockIdx.x == 0 && blockIdx.y == 0);
+  if (j.n <= 0) return;
+  if (blockIdx.x & 1)
+    append_values<kE4M3, kThreads, kRows>(p, j, s_amax);
+  else
+    append_keys<kE4M3, kThreads, kRows>(p, j, s_amax, s_bound);
 }
 
 }  // namespace pap

@@ -135,14 +135,15 @@ def test_binding_refuses_before_the_library():
 
 
 def test_binding_checks_each_tensor():
-    dev = torch.device("cpu")
     t = torch.zeros(2, 3, dtype=torch.int32)
-    la._tensor("t", t, (torch.int32,), (2, None), dev)
-    for bad in (t.float(), t[0], t[:, :2], torch.zeros(3, 3, dtype=torch.int32)):
+    la._tensor("t", t, torch.int32, (2, 3), -1)  # device index -1: CPU
+    for bad in (t.float(), t[0], t[:, :2], t.T.contiguous().T, torch.zeros(3, 3, dtype=torch.int32)):
         with pytest.raises(ValueError, match="t: "):
-            la._tensor("t", bad, (torch.int32,), (2, None), dev)
-    with pytest.raises(ValueError, match="on cuda:0 expected"):
-        la._tensor("t", t, (torch.int32,), (2, None), torch.device("cuda", 0))
+            la._tensor("t", bad, torch.int32, (2, 3), -1)
+    with pytest.raises(ValueError, match="on CUDA device 0 expected"):
+        la._tensor("t", t, torch.int32, (2, 3), 0)
+    with pytest.raises(ValueError, match="3 dimensions expected"):
+        la._dim("t", t, 3)
 
 
 # ---- the statements the GPU tests rely on

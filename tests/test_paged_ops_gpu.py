@@ -230,6 +230,33 @@ def test_append_steps_equal_one_append_but_for_subnormals(T):
         assert (x - y).abs().max() <= 2.0 ** -9  # two roundings, half a subnormal step each
 
 
+@pytest.mark.parametrize("page,Hkv,B,T", [(64, 8, 37, 300), (128, 4, 90, 500), (64, 1, 200, 400), (192, 3, 70, 700), (512, 2, 60, 1500)])
+def test_append_of_a_large_batch_equals_its_parts(page, Hkv, B, T):
+    """A ragged batch of many blocks at once, and sequence by sequence: the same bits. (Large and
+    small appends run on different kernels; the parts are those test_append checks.)"""
+    g = gen(T)
+    lens = [int(x) for x in torch.randint(0, 3 * page, (B,), generator=g)]
+    new = [int(x) for x in torch.randint(0, T + 1, (B,), generator=g)]
+    lens[0], new[0], lens[1], new[1], lens[2], new[2] = 0, 5, 0, T, page, T
+    s = append_state("e4m3", page, Hkv, T, lens, new, 12)
+    s["table"][5, 0] = -1 if lens[5] < page and new[5] else s["table"][5, 0]
+    rope = la.llama_attn_rope_table_build(s["table"].shape[1] * page, D, THETA)
+    a = run_append("e4m3", s, lens, rope, s["k"].cuda(), s["v"].cuda(), new)
+    bad = la.DEVERR_BLOCK_TABLE if lens[5] < page and new[5] else 0
+    assert la.llama_attn_get_device_error() == bad
+    out = []
+    for b in range(B):
+        one = dict(s, B=1, table=s["table"][b:b + 1])
+        d = run_append("e4m3", one, lens[b:b + 1], rope, s["k"][b:b + 1].cuda(), s["v"][b:b + 1].cuda(), new[b:b + 1])
+        s["pools"], s["scales"] = [x.cpu() for x in d["pools"]], [x.cpu() for x in d["scales"]]
+        s["bounds"] = d["bounds"].cpu()
+        out += d["out_lens"].tolist()
+    assert la.llama_attn_get_device_error() == bad
+    assert a["out_lens"].tolist() == out
+    for x, y in zip(a["pools"] + a["scales"] + [a["bounds"]], s["pools"] + s["scales"] + [s["bounds"]]):
+        assert torch.equal(x.cpu(), y)
+
+
 def test_append_leaves_refused_sequences_alone():
     page, Hkv, T = 64, 1, 4
     lens, new = [-1, 10, 126, 5], [4, 9, 4, 4]  # negative length, more than T, past the table, fine
