@@ -545,12 +545,13 @@ def _call(fn, index, stream, *args):
     one) and that device's current stream, or on ``stream``."""
     import torch
     if stream is None:
-        raw = torch.cuda.current_stream(index).cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(index)  # torch.cuda.current_stream(index).cuda_stream
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on device {index}")
     else:
-        _require(stream.device.index == index, f"stream is on {stream.device}, the tensors are on device {index}")
         raw = stream.cuda_stream
     f = getattr(_lib or lib(), fn)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = f(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -563,13 +564,32 @@ def _pool(kpages, vpages, scales, dtypes, D, index):
     """Checks a page pool with its scales; (n_pages, Hkv, page_size)."""
     import torch
     n_pages, Hkv, page_size, _ = shape = _dim("kpages", kpages, 4)
-    _require(kpages.dtype in dtypes, f"kpages: {kpages.dtype} pages are not supported here")
-    _tensor("kpages", kpages, kpages.dtype, (n_pages, Hkv, page_size, D), index)
-    _tensor("vpages", vpages, kpages.dtype, shape, index)
+    dtype = kpages.dtype
+    if dtype not in dtypes or shape[3] != D:
+        raise ValueError(f"kpages: {dtypes} pages with rows of {D} expected, got {tuple(shape)} {dtype}")
+    _tensor("kpages", kpages, dtype, shape, index)
+    _tensor("vpages", vpages, dtype, shape, index)
     if scales:
-        _tensor("k_scales", scales[0], torch.float32, (n_pages, Hkv), index)
-        _tensor("v_scales", scales[1], torch.float32, (n_pages, Hkv), index)
+        shape = (n_pages, Hkv)
+        _tensor("k_scales", scales[0], torch.float32, shape, index)
+        _tensor("v_scales", scales[1], torch.float32, shape, index)
     return n_pages, Hkv, page_size
+
+
+def _kv_strides(k, v, index):
+    """(row stride, batch stride) in elements that k and v [B, T, Hkv, D] share."""
+    import torch
+    for name, t in (("k", k), ("v", v)):
+        if t.get_device() != index or t.dtype is not torch.bfloat16 or t.shape != k.shape:
+            raise ValueError(f"{name}: bfloat16 tensor of shape {tuple(k.shape)} on CUDA device {index} expected, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    B, T, Hkv, D = k.shape
+    sb, st, sh, sd = k.stride()
+    vb, vt, vh, vd = v.stride()
+    _require((sd == vd == 1 or D == 1) and (sh == vh == D or Hkv == 1),
+             "k and v: the heads of a token must be contiguous")
+    _require((st == vt or T == 1) and (sb == vb or B == 1), "k and v must have the same strides")
+    return st if T > 1 else Hkv * D, sb if B > 1 else 0
 
 
 def _append(fn, k, v, kpages, vpages, scales, block_table, cache_lens, rope_table, new_lens, kbounds, out_lens, dtypes,
@@ -578,21 +598,16 @@ def _append(fn, k, v, kpages, vpages, scales, block_table, cache_lens, rope_tabl
     i32 = torch.int32
     index = _cuda_index("k", k)
     B, T, Hkv, D = shape = _dim("k", k, 4)
-    for name, t in (("k", k), ("v", v)):
-        if t.get_device() != index or t.dtype is not torch.bfloat16 or t.shape != shape:
-            raise ValueError(f"{name}: bfloat16 tensor of shape {tuple(shape)} on CUDA device {index} expected, got "
-                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    sb, st, sh, sd = k.stride()
     if k.is_contiguous() and v.is_contiguous():
-        st, sb = Hkv * D, T * Hkv * D
+        _tensor("k", k, torch.bfloat16, shape, index)
+        _tensor("v", v, torch.bfloat16, shape, index)
+        st = Hkv * D
+        sb = T * st
     else:
-        vb, vt, vh, vd = v.stride()
-        _require((sd == vd == 1 or D == 1) and (sh == vh == D or Hkv == 1),
-                 "k and v: the heads of a token must be contiguous")
-        _require((st == vt or T == 1) and (sb == vb or B == 1), "k and v must have the same strides")
-        st, sb = st if T > 1 else Hkv * D, sb if B > 1 else 0
+        st, sb = _kv_strides(k, v, index)
     n_pages, pool_heads, page_size = _pool(kpages, vpages, scales, dtypes, D, index)
-    _require(pool_heads == Hkv, f"kpages: {Hkv} KV heads expected, got {pool_heads}")
+    if pool_heads != Hkv:
+        raise ValueError(f"kpages: {Hkv} KV heads expected, got {pool_heads}")
     max_blocks = _dim("block_table", block_table, 2)[1]
     _tensor("block_table", block_table, i32, (B, max_blocks), index)
     _tensor("cache_lens", cache_lens, i32, (B,), index)
@@ -662,8 +677,8 @@ def _decode_runs(fn, q, kpages, vpages, scales, block_table, block_ids, cache_le
     if workspace is None:
         workspace = torch.empty(max(1, llama_attn_decode_runs_workspace_size(B, Hq, Hkv, D)), dtype=torch.uint8,
                                 device=q.device)
-    _require(workspace.get_device() == index and workspace.is_contiguous(),
-             f"workspace: contiguous tensor on CUDA device {index} expected")
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous tensor on CUDA device {index} expected")
     pools = (q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), *[t.data_ptr() for t in scales],
              block_table.data_ptr())
     sizes = (out.data_ptr(), lse, B, Hq, Hkv, D, page_size, max_blocks, n_pages)

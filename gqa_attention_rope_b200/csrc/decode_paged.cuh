@@ -43,28 +43,37 @@ namespace la {
 namespace dpg {
 
 constexpr int ROWS = 64;                  // cache rows of a stage
-constexpr int NCW = 4;                    // compute warps: 16 rows of a stage each
-constexpr int NTHREADS = (NCW + 1) * 32;  // and the producer warp
+constexpr int NRW = 4;                    // row groups: 16 rows of a stage each
 constexpr float kLift = 7.f;              // P of the greatest row: 2^7
 constexpr int MAX_CTAS = 512;             // runs (and twice as many partial results) the workspace holds
 
-template <bool kE4M3>
+// kWide: more than 8 query heads per KV head, two tiles of 8 (NT). Four compute
+// warps have 16 rows of a stage each, one more warp loads.
+template <bool kE4M3, bool kWide>
 struct Tile {
+  static constexpr int NT = kWide ? 2 : 1;
+  static constexpr int NCW = NRW;
+  static constexpr int NTHREADS = (NCW + 1) * 32;
+  // CTAs per SM. For two tiles of E4M3 (one 131072-row sequence under 128
+  // heads): 2 with the query in registers 56 us, 3 with it in shared memory
+  // (128 registers, 4 stages each) 76 us, 2 of eight compute warps with a tile
+  // each (every code converted twice) 63 us.
+  static constexpr int CTAS = 2;
+  static constexpr bool Q_REGS = kE4M3 || !kWide;  // query fragments in registers (two tiles of two bf16 terms: 64)
   static constexpr uint32_t HALF = ROWS * 128;                    // 64 rows x 128 bytes
   static constexpr uint32_t TENSOR = kE4M3 ? HALF : 2 * HALF;     // K or V of a stage
   static constexpr uint32_t STAGE = 2 * TENSOR;
-  static constexpr int NSTAGE = kE4M3 ? 6 : 3;                    // 96 KB: two CTAs per SM
+  static constexpr int NSTAGE = kE4M3 ? 6 : 3;                    // 192 KB of stages per SM
   // One region for two uses that never overlap in time: the query rows (f16,
-  // or two bf16 terms) until every warp holds its fragments, and the merge
-  // scratch (two warps x 8 heads x 128 float) at a segment's end.
+  // or two bf16 terms) until a segment's last product, and the merge scratch
+  // (two warps x 8 heads x 64 channels, float) behind it.
   static constexpr uint32_t OFF_Q = NSTAGE * STAGE;
   static constexpr uint32_t OFF_SCR = OFF_Q;
   static constexpr uint32_t Q_ROW = 264;                          // bytes: 128 16-bit values, 8 bytes of padding
-  static constexpr uint32_t OFF_META = OFF_Q + (kE4M3 ? 8192 : 32 * Q_ROW);
+  static constexpr uint32_t OFF_META = OFF_Q + (kE4M3 || !kWide ? 16 : 32) * Q_ROW;
   static constexpr uint32_t OFF_BAR = OFF_META + NSTAGE * 16;
   static constexpr uint32_t OFF_ML = OFF_BAR + 128;               // per warp and head: m, l
-  static constexpr uint32_t OFF_FREQ = OFF_ML + NCW * 16 * 8;     // theta_k in float64
-  static constexpr uint32_t OFF_CS = OFF_FREQ + 64 * 8;           // (cos, sin) row of the segment
+  static constexpr uint32_t OFF_CS = OFF_ML + NCW * 16 * 8;       // (cos, sin) row of the segment
   static constexpr uint32_t OFF_QS = OFF_CS + 64 * 8;             // per head: factor of the query row
   static constexpr uint32_t SMEM_ALLOC = OFF_QS + 64 + 1024;
 };
@@ -80,35 +89,35 @@ struct Params {
   const float* kscales;       // [n_pages, Hkv], E4M3 only
   const float* vscales;
   float scale_log2;
-  double rope_theta;
+  RopeFreqs freqs;
   uint16_t* out;              // [B, Hq, 128] bf16
   float* lse;                 // [B, Hq] or null
   float* part_o;              // [2 * MAX_CTAS][G][128]
   float2* part_ml;            // [2 * MAX_CTAS][G]
-  int64_t* prefix;            // [B + 1] units before each sequence
+  int* prefix;                // [B + 1] units before each sequence
+  int4* ends;                 // [MAX_CTAS] (sequence, KV head, first run) of a pair that ends in a run but began before
   unsigned int epoch;
 };
 
 // Stages of one (sequence, KV head).
 template <bool kSparse>
-__device__ __forceinline__ int64_t stages_of(const Params& p, int b) {
+__device__ __forceinline__ int stages_of(const Params& p, int b) {
   const int len = p.lens[b];
   if (len <= 0 || len > static_cast<int64_t>(p.max_blocks) * p.page_size) return 0;
   if constexpr (kSparse) {
     const int nb = (len + p.page_size - 1) / p.page_size;
-    return static_cast<int64_t>(min(nb, p.n_sel)) * (p.page_size / ROWS);
+    return min(nb, p.n_sel) * (p.page_size / ROWS);
   }
   return (len + ROWS - 1) / ROWS;
 }
 
 // Position of a unit in the order (sequence, KV head, stage).
 struct Cursor {
-  int b, g;
-  int64_t s, nst;
+  int b, g, s, nst;
 };
 
 template <bool kSparse>
-__device__ __forceinline__ void advance(const Params& p, Cursor& c, int64_t by) {
+__device__ __forceinline__ void advance(const Params& p, Cursor& c, int by) {
   c.s += by;
   while (c.b < p.B && c.s >= c.nst) {
     c.s -= c.nst;
@@ -118,10 +127,17 @@ __device__ __forceinline__ void advance(const Params& p, Cursor& c, int64_t by) 
   }
 }
 
-// Units [lo, hi) of run i of n over `total` units.
-__device__ __forceinline__ int64_t run_start(int64_t total, int64_t n, int64_t i) { return total * i / n; }
-// The run that holds unit u.
-__device__ __forceinline__ int64_t run_of(int64_t total, int64_t n, int64_t u) { return ((u + 1) * n - 1) / total; }
+// The cut of `total` units into n <= total runs: the first total % n of them
+// have one unit more than the others.
+struct Cut {
+  int q, r;
+  __device__ __forceinline__ Cut(int total, int n) : q(total / n), r(total - total / n * n) {}
+  __device__ __forceinline__ int start(int run) const { return q * run + min(run, r); }
+  __device__ __forceinline__ int run_of(int u) const {
+    const int big = r * (q + 1);
+    return u < big ? u / (q + 1) : r + (u - big) / q;
+  }
+};
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -151,13 +167,28 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Sequences without rows: zeros, dealt out over the CTAs; `n` threads of each.
+template <bool kSparse>
+__device__ __forceinline__ void clear_empty(const Params& p, int n) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (stages_of<kSparse>(p, b) > 0) continue;
+    const int len = p.lens[b];
+    if (threadIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(p.max_blocks) * p.page_size))
+      raise_error(LLAMA_ATTN_DEVERR_CACHE_LEN);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(b) * p.Hq * 128);
+    for (int i = threadIdx.x; i < p.Hq * 64; i += n) dst[i] = 0u;
+    if (p.lse)
+      for (int i = threadIdx.x; i < p.Hq; i += n) p.lse[static_cast<int64_t>(b) * p.Hq + i] = -INFINITY;
+  }
+}
+
 // kWide: more than 8 query heads per KV head (two tiles of 8).
 template <bool kE4M3, bool kSparse, bool kWide>
-__global__ void __launch_bounds__(NTHREADS, 2)
+__global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, kWide>::CTAS))
     decode_runs_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const Params p) {
-  using T = Tile<kE4M3>;
-  constexpr int NT = kWide ? 2 : 1;
+  using T = Tile<kE4M3, kWide>;
+  constexpr int NT = T::NT, NCW = T::NCW, NTHREADS = T::NTHREADS;
   constexpr int NQ = kE4M3 ? 1 : 2;  // terms of Q
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -167,9 +198,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wc{p.epoch};
 
-  __shared__ int64_t s_start_s, s_start_nst;
-  __shared__ int s_start_b, s_start_g;
-  __shared__ int64_t s_part[NTHREADS];
+  __shared__ int4 s_start;
+  __shared__ int s_part[NTHREADS];
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::NSTAGE; ++s) {
@@ -180,151 +210,174 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (threadIdx.x < 64)
-    reinterpret_cast<double*>(smem + T::OFF_FREQ)[threadIdx.x] =
-        pow(p.rope_theta, -2.0 * static_cast<double>(threadIdx.x) / 128.0);
+  grid_launch_dependents();
+  grid_dependency_wait();
   // Units before this thread's share of the sequences, and in all: thread i
   // takes sequences [i * per, (i + 1) * per).
   const int per = (p.B + NTHREADS - 1) / NTHREADS;
   const int my0 = min(p.B, static_cast<int>(threadIdx.x) * per), my1 = min(p.B, my0 + per);
   {
-    int64_t sum = 0;
+    int sum = 0;
     for (int b = my0; b < my1; ++b) sum += stages_of<kSparse>(p, b) * p.Hkv;
     s_part[threadIdx.x] = sum;
   }
   __syncthreads();
-  int64_t before = 0, total = 0;
+  int before = 0, total = 0;
   for (int i = 0; i < NTHREADS && i * per < p.B; ++i) {
     if (i == static_cast<int>(threadIdx.x)) before = total;
     total += s_part[i];
   }
   if (my0 < p.B && blockIdx.x == 0) {  // the joining kernel reads these
-    int64_t at = before;
+    int at = before;
     for (int b = my0; b < my1; ++b) {
       p.prefix[b] = at;
       at += stages_of<kSparse>(p, b) * p.Hkv;
     }
     if (my1 == p.B) p.prefix[p.B] = at;
   }
-  if (total == 0) return;
-  const int64_t n_runs = min(static_cast<int64_t>(gridDim.x), total);
-  if (blockIdx.x >= n_runs) return;
-  const int64_t u0 = run_start(total, n_runs, blockIdx.x), u1 = run_start(total, n_runs, blockIdx.x + 1);
+  if (threadIdx.x == 0) p.ends[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  const int n_runs = min(static_cast<int>(gridDim.x), total);
+  if (static_cast<int>(blockIdx.x) >= n_runs) {
+    clear_empty<kSparse>(p, NTHREADS);
+    return;
+  }
+  const Cut cut(total, n_runs);
+  const int u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
   if (my0 < my1 && before <= u0 && u0 < before + s_part[threadIdx.x]) {  // one thread finds the start
-    int64_t at = before;
+    int at = before;
     for (int b = my0; b < my1; ++b) {
-      const int64_t nst = stages_of<kSparse>(p, b), n = nst * p.Hkv;
+      const int nst = stages_of<kSparse>(p, b), n = nst * p.Hkv;
       if (u0 < at + n) {
-        s_start_b = b;
-        s_start_g = static_cast<int>((u0 - at) / nst);
-        s_start_s = (u0 - at) % nst;
-        s_start_nst = nst;
+        const int g = (u0 - at) / nst;
+        s_start = make_int4(b, g, u0 - at - g * nst, nst);
         break;
       }
       at += n;
     }
   }
   __syncthreads();
-  Cursor cur{s_start_b, s_start_g, s_start_s, s_start_nst};
+  Cursor cur{s_start.x, s_start.y, s_start.z, s_start.w};
 
   if (warp == NCW) {
     // ------------------------------------------------------------ producer
-    // The lanes resolve the next 32 units (block id, page, scales: dependent
-    // loads) while lane 0 issues the copies of the present 32.
+    // The lanes resolve 32 units at a time, in three steps that depend on one
+    // another's loads: chosen block ids, pages, scales. Each step runs a batch
+    // ahead of the next, so that its loads have a batch's time to arrive.
     const int rpp = p.page_size;
-    const int64_t pool_rows = static_cast<int64_t>(p.n_pages) * p.Hkv * rpp;
     Cursor c = cur;
-    int64_t u = u0 + lane;
+    int u = u0 + lane;
     if (lane > 0) advance<kSparse>(p, c, lane);
+    struct Ids {
+      Cursor c;
+      int len, id, prev;  // len 0: no unit
+    };
+    struct Page {
+      int g, n, nvalid, page;  // first cache row, rows below len (0: nothing to load)
+    };
     struct Unit {
-      int row, nvalid;   // first row in the pool, rows below len (0: nothing to load)
+      int row, nvalid;  // first row in the pool
       float ks, vs;
     };
-    auto resolve = [&]() {
-      Unit r{0, 0, 1.f, 1.f};
+    auto load_ids = [&]() {  // and on to the next batch
+      Ids r{c, 0, 0, -2};
       if (u >= u1) return r;
-      const int len = p.lens[c.b];
-      int n;  // the unit's first cache row
+      r.len = p.lens[c.b];
       if constexpr (kSparse) {
-        const int spp = rpp / ROWS;
-        const int e = static_cast<int>(c.s) / spp;
+        const int e = c.s / (rpp / ROWS);
         const int32_t* ids = p.block_ids + (static_cast<int64_t>(c.b) * p.Hkv + c.g) * p.n_sel;
-        const int id = ids[e], prev = e > 0 ? ids[e - 1] : -2;
-        const int nb = (len + rpp - 1) / rpp;
+        r.id = ids[e];
+        if (e > 0) r.prev = ids[e - 1];
+      }
+      u += 32;
+      if (u < u1) advance<kSparse>(p, c, 32);
+      return r;
+    };
+    auto load_page = [&](const Ids& a) {
+      Page r{a.c.g, 0, 0, 0};
+      if (a.len == 0) return r;
+      if constexpr (kSparse) {
+        const int spp = rpp / ROWS, e = a.c.s / spp, nb = (a.len + rpp - 1) / rpp;
         // ascending, no id twice, -1 only behind the last one
-        const bool use = id >= 0 && id < nb && (e == 0 || (prev >= 0 && prev < id));
+        const bool use = a.id >= 0 && a.id < nb && (e == 0 || (a.prev >= 0 && a.prev < a.id));
         if (!use) {
-          if (id != -1) raise_error(LLAMA_ATTN_DEVERR_BLOCK_IDS);
+          if (a.id != -1) raise_error(LLAMA_ATTN_DEVERR_BLOCK_IDS);
           return r;
         }
-        n = id * rpp + (static_cast<int>(c.s) - e * spp) * ROWS;
-        if (n >= len) return r;
+        r.n = a.id * rpp + (a.c.s - e * spp) * ROWS;
+        if (r.n >= a.len) return r;
       } else {
-        n = static_cast<int>(c.s) * ROWS;
+        r.n = a.c.s * ROWS;
       }
-      r.nvalid = min(ROWS, len - n);
-      const int page = p.block_table[static_cast<int64_t>(c.b) * p.max_blocks + n / rpp];
-      if (page < 0 || page >= p.n_pages) {
+      r.nvalid = min(ROWS, a.len - r.n);
+      r.page = p.block_table[static_cast<int64_t>(a.c.b) * p.max_blocks + r.n / rpp];
+      return r;
+    };
+    auto load_scales = [&](const Page& a) {
+      Unit r{0, a.nvalid, 1.f, 1.f};
+      if (a.nvalid == 0) return r;
+      if (a.page < 0 || a.page >= p.n_pages) {
         raise_error(LLAMA_ATTN_DEVERR_BLOCK_TABLE);
-        r.row = static_cast<int>(pool_rows);  // past the pool: the copy reads zeros
+        r.row = p.n_pages * p.Hkv * rpp;  // past the pool: the copy reads zeros
       } else {
-        r.row = (page * p.Hkv + c.g) * rpp + n % rpp;
+        const int ph = a.page * p.Hkv + a.g;
+        r.row = ph * rpp + a.n % rpp;
         if constexpr (kE4M3) {
-          r.ks = __ldg(p.kscales + static_cast<int64_t>(page) * p.Hkv + c.g);
-          r.vs = __ldg(p.vscales + static_cast<int64_t>(page) * p.Hkv + c.g);
+          r.ks = __ldg(p.kscales + ph);
+          r.vs = __ldg(p.vscales + ph);
         }
       }
       return r;
     };
-    const int n_units = static_cast<int>(u1 - u0);
-    Unit next = resolve();
+    const int n_units = u1 - u0;
+    Page page = load_page(load_ids());
+    Ids ids = load_ids();
     bool alive = true;
     int done = 0;
     for (int i0 = 0; i0 < n_units && alive; i0 += 32) {
-      const Unit now = next;
-      u += 32;
-      if (u < u1) advance<kSparse>(p, c, 32);
-      next = resolve();
-      // a scale outside [2^-100, 2^119] would leave the range of the exponent trick
-      const float vs = fminf(fmaxf(now.vs, 7.888609e-31f), 6.646140e35f);
-      const float lv = kE4M3 ? __log2f(vs) : 0.f, iv = kE4M3 ? 1.f / vs : 1.f;
+      const Unit now = load_scales(page);
       const int m = min(32, n_units - i0);
       for (int j = 0; j < m; ++j) {
         const int row = __shfl_sync(0xffffffffu, now.row, j);
         const int nvalid = __shfl_sync(0xffffffffu, now.nvalid, j);
-        const float ks = __shfl_sync(0xffffffffu, now.ks, j);
-        const float l2 = __shfl_sync(0xffffffffu, lv, j), inv = __shfl_sync(0xffffffffu, iv, j);
         const uint32_t st = static_cast<uint32_t>(i0 + j) % T::NSTAGE;
         const int use = (i0 + j) / T::NSTAGE;
         int ok = 1;
         if (lane == 0) {
           ok = use == 0 || mbar_wait(empty(st), (use - 1) & 1, wc);
-          if (ok) {
+          if (ok && nvalid > 0) {
             const uint32_t dst = sbase + st * T::STAGE;
-            if (nvalid > 0) {
-              if constexpr (kE4M3) {
-                tma_load_2d(dst, &tm_k, full(st), 0, row);
-                tma_load_2d(dst + T::TENSOR, &tm_v, full(st), 0, row);
-              } else {
-                tma_load_2d(dst, &tm_k, full(st), 0, row);
-                tma_load_2d(dst + T::HALF, &tm_k, full(st), 64, row);
-                tma_load_2d(dst + T::TENSOR, &tm_v, full(st), 0, row);
-                tma_load_2d(dst + T::TENSOR + T::HALF, &tm_v, full(st), 64, row);
-              }
+            if constexpr (kE4M3) {
+              tma_load_2d(dst, &tm_k, full(st), 0, row);
+              tma_load_2d(dst + T::TENSOR, &tm_v, full(st), 0, row);
+            } else {
+              tma_load_2d(dst, &tm_k, full(st), 0, row);
+              tma_load_2d(dst + T::HALF, &tm_k, full(st), 64, row);
+              tma_load_2d(dst + T::TENSOR, &tm_v, full(st), 0, row);
+              tma_load_2d(dst + T::TENSOR + T::HALF, &tm_v, full(st), 64, row);
             }
-            *reinterpret_cast<float4*>(smem + T::OFF_META + st * 16) =
-                make_float4(__int_as_float(nvalid), ks, l2, inv);
-            if (nvalid > 0)
-              mbar_arrive_expect_tx(full(st), T::STAGE);
-            else
-              mbar_arrive(full(st));
           }
+        }
+        // the scales are needed only now, with the copies on their way; a value
+        // scale outside [2^-100, 2^119] would leave the exponent's range
+        const float ks = __shfl_sync(0xffffffffu, now.ks, j);
+        const float vs = fminf(fmaxf(__shfl_sync(0xffffffffu, now.vs, j), 7.888609e-31f), 6.646140e35f);
+        if (lane == 0 && ok) {
+          *reinterpret_cast<float4*>(smem + T::OFF_META + st * 16) =
+              make_float4(__int_as_float(nvalid), ks, kE4M3 ? __log2f(vs) : 0.f, kE4M3 ? 1.f / vs : 1.f);
+          if (nvalid > 0)
+            mbar_arrive_expect_tx(full(st), T::STAGE);
+          else
+            mbar_arrive(full(st));
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
           alive = false;
           break;
         }
         ++done;
+        if (j == min(3, m - 1)) {  // the steps for the batches to come, behind the first copies
+          page = load_page(ids);
+          ids = load_ids();
+        }
       }
     }
     if (lane == 0)  // copies in flight land before the CTA's shared memory goes
@@ -336,58 +389,70 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   // -------------------------------------------------------------- compute warps
   const int gq = lane >> 2, t = lane & 3;
   const int G = p.G;
-  auto bar = [] { asm volatile("bar.sync 1, %0;" ::"r"(NCW * 32) : "memory"); };
-  uint32_t qb[NQ][NT][8][2];
-  float qf[NT][2];
-  float m[NT][2], l[NT][2];
+  auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory"); };
+  uint32_t qb[T::Q_REGS ? NQ : 1][T::Q_REGS ? NT : 1][8][2];
+  float qf[NT][2], m[NT][2], l[NT][2];
   float o[NT][8][4];
+  // B fragment of the query for k step c, from shared memory; q_frag: from where the kernel keeps it.
+  auto q_read = [&](int term, int nt, int c, uint32_t& b0, uint32_t& b1) {
+    const uint8_t* row = smem + T::OFF_Q + (8 * NT * term + 8 * nt + gq) * T::Q_ROW + 32 * c;
+    if constexpr (kE4M3) {  // codes 4t .. 4t+3 of a 16-byte chunk
+      const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * t);
+      b0 = v.x, b1 = v.y;
+    } else {
+      b0 = *reinterpret_cast<const uint32_t*>(row + 4 * t);
+      b1 = *reinterpret_cast<const uint32_t*>(row + 16 + 4 * t);
+    }
+  };
+  auto q_frag = [&](int term, int nt, int c, uint32_t& b0, uint32_t& b1) {
+    if constexpr (T::Q_REGS)
+      b0 = qb[term][nt][c][0], b1 = qb[term][nt][c][1];
+    else
+      q_read(term, nt, c, b0, b1);
+  };
 
   // The rotated query rows of (b, g) as B fragments of the score product.
   auto load_query = [&]() {
     float2* cs_row = reinterpret_cast<float2*>(smem + T::OFF_CS);
     if (threadIdx.x < 64) {
       double sn, cs;
-      sincos(static_cast<double>(p.lens[cur.b] + p.q_pos_offset) *
-                 reinterpret_cast<const double*>(smem + T::OFF_FREQ)[threadIdx.x], &sn, &cs);
+      sincos(static_cast<double>(p.lens[cur.b] + p.q_pos_offset) * p.freqs.theta[threadIdx.x], &sn, &cs);
       cs_row[threadIdx.x] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
     }
+    uint2 u[2 * NT];  // a warp stages two heads of each tile
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      const int h = warp + i * NCW;
+      u[i] = make_uint2(0u, 0u);
+      if (h < G)
+        u[i] = *reinterpret_cast<const uint2*>(p.q + (static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h) * 128 + 4 * lane);
+    }
     bar();
-    for (int h = warp; h < 8 * NT; h += NCW) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (h < G) {
-        const uint2 u = *reinterpret_cast<const uint2*>(
-            p.q + (static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h) * 128 + 4 * lane);
-        const float4 cs = reinterpret_cast<const float4*>(cs_row)[lane];
-        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
-        x[0] = a.x * cs.x - a.y * cs.y;
-        x[1] = a.x * cs.y + a.y * cs.x;
-        x[2] = b.x * cs.z - b.y * cs.w;
-        x[3] = b.x * cs.w + b.y * cs.z;
-      }
+    const float4 cs = reinterpret_cast<const float4*>(cs_row)[lane];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      const int h = warp + i * NCW;
+      const float2 a = unpack_bf16x2(u[i].x), b = unpack_bf16x2(u[i].y);
+      const float x[4] = {a.x * cs.x - a.y * cs.y, a.x * cs.y + a.y * cs.x, b.x * cs.z - b.y * cs.w,
+                          b.x * cs.w + b.y * cs.z};
       uint8_t* row = smem + T::OFF_Q + h * T::Q_ROW + 8 * lane;
       if constexpr (kE4M3) {
-        float am = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, s));
-        // bring the row's greatest magnitude to [0.5, 1): exact, and undone in the scores' factor
-        const int e = am > 0.f ? min(max(static_cast<int>(__float_as_uint(am) >> 23) - 126, -100), 120) : 0;
+        const float am = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+        // bring the row's greatest magnitude (which orders like its bits) to
+        // [0.5, 1): exact, and undone in the scores' factor
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+        const int e = bits ? min(max(static_cast<int>(bits >> 23) - 126, -100), 120) : 0;
         const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         *reinterpret_cast<uint2*>(row) = make_uint2(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f));
         if (lane == 0)
           reinterpret_cast<float*>(smem + T::OFF_QS)[h] =
               p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       } else {
-        float r[4];
-        uint32_t hi[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-          const float2 v = unpack_bf16x2(hi[i]);
-          r[2 * i] = x[2 * i] - v.x;
-          r[2 * i + 1] = x[2 * i + 1] - v.y;
-        }
+        const uint32_t hi[2] = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+        const float2 v = unpack_bf16x2(hi[0]), w = unpack_bf16x2(hi[1]);
         *reinterpret_cast<uint2*>(row) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(row + 16 * T::Q_ROW) = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+        *reinterpret_cast<uint2*>(row + 8 * NT * T::Q_ROW) =
+            make_uint2(pack_bf16x2(x[0] - v.x, x[1] - v.y), pack_bf16x2(x[2] - w.x, x[3] - w.y));
       }
     }
     bar();
@@ -395,102 +460,94 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        if constexpr (kE4M3)
-          qf[nt][e] = reinterpret_cast<const float*>(smem + T::OFF_QS)[8 * nt + 2 * t + e];
-        else
-          qf[nt][e] = p.scale_log2;
+        qf[nt][e] = kE4M3 ? reinterpret_cast<const float*>(smem + T::OFF_QS)[8 * nt + 2 * t + e] : p.scale_log2;
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-#pragma unroll
-        for (int term = 0; term < NQ; ++term) {
-          const uint8_t* row = smem + T::OFF_Q + (16 * term + 8 * nt + gq) * T::Q_ROW + 32 * c;
-          if constexpr (kE4M3) {  // codes 4t .. 4t+3 of a 16-byte chunk
-            const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * t);
-            qb[term][nt][c][0] = v.x;
-            qb[term][nt][c][1] = v.y;
-          } else {
-            qb[term][nt][c][0] = *reinterpret_cast<const uint32_t*>(row + 4 * t);
-            qb[term][nt][c][1] = *reinterpret_cast<const uint32_t*>(row + 16 + 4 * t);
-          }
-        }
+      for (int c = 0; c < 8; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][c][e] = 0.f;
-      }
+    }
+    if constexpr (T::Q_REGS) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int term = 0; term < NQ; ++term) q_read(term, nt, c, qb[term][nt][c][0], qb[term][nt][c][1]);
     }
   };
 
   // Joins the four warps' results of the segment that ends here, and writes it.
-  auto finish = [&](int64_t first_unit, int64_t last_unit) {
+  auto finish = [&](int first_unit, int last_unit) {
     float2* ml = reinterpret_cast<float2*>(smem + T::OFF_ML);  // [warp][head]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
-        if (gq == 0) ml[warp * 16 + 8 * nt + 2 * t + e] = make_float2(m[nt][e], l[nt][e]);
+        float& s = l[nt][e];
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+        if (gq == 0) ml[warp * 16 + 8 * nt + 2 * t + e] = make_float2(m[nt][e], s);
       }
     bar();
-    float M[NT][2], L[NT][2];
+    float4* scr = reinterpret_cast<float4*>(smem + T::OFF_SCR);
+    const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
+    if (first_unit < u0 && last_unit <= u1 && threadIdx.x == 0)
+      p.ends[blockIdx.x] = make_int4(cur.b, cur.g, cut.run_of(first_unit), 0);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float M[2], L[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = -INFINITY, sum = 0.f;
+        float2 v[NCW];
 #pragma unroll
-        for (int w = 0; w < NCW; ++w) mx = fmaxf(mx, ml[w * 16 + 8 * nt + 2 * t + e].x);
+        for (int w = 0; w < NCW; ++w) v[w] = ml[w * 16 + 8 * nt + 2 * t + e];
+        M[e] = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+        L[e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < NCW; ++w) {
-          const float2 v = ml[w * 16 + 8 * nt + 2 * t + e];
-          if (v.x > -INFINITY || v.x != v.x) sum += v.y * ex2_approx(v.x - mx);
-          else sum += v.y;  // no row: zero; a NaN stays one
-        }
-        M[nt][e] = mx;
-        L[nt][e] = sum;
-        const float f = m[nt][e] == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mx);
+        for (int w = 0; w < NCW; ++w) L[e] += v[w].x == -INFINITY ? v[w].y : v[w].y * ex2_approx(v[w].x - M[e]);  // no row: 0 (or a NaN)
+        const float f = m[nt][e] == -INFINITY ? 1.f : ex2_approx(m[nt][e] - M[e]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           o[nt][c][e] *= f;
           o[nt][c][2 + e] *= f;
         }
       }
-    float* scr = reinterpret_cast<float*>(smem + T::OFF_SCR);
+      // the scratch holds two warps' channels of half the chunks
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      for (int c0 = 0; c0 < 8; c0 += 4) {
 #pragma unroll
-      for (int half = NCW / 2; half > 0; half >>= 1) {
-        if (nt > 0 || half < NCW / 2) bar();  // the scratch of the step before has been read
-        if (warp >= half && warp < 2 * half) {
-          float4* dst = reinterpret_cast<float4*>(scr + (warp - half) * 1024);
+        for (int half = NCW / 2; half > 0; half >>= 1) {
+          if (nt > 0 || c0 > 0 || half < NCW / 2) bar();  // the scratch of the step before has been read
+          if (warp >= half && warp < 2 * half) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) dst[c * 32 + lane] = make_float4(o[nt][c][0], o[nt][c][1], o[nt][c][2], o[nt][c][3]);
-        }
-        bar();
-        if (warp < half) {
-          const float4* src = reinterpret_cast<const float4*>(scr + warp * 1024);
+            for (int c = 0; c < 4; ++c) {
+              const float* x = o[nt][c0 + c];
+              scr[((warp - half) * 4 + c) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          bar();
+          if (warp < half) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 v = src[c * 32 + lane];
-            o[nt][c][0] += v.x, o[nt][c][1] += v.y, o[nt][c][2] += v.z, o[nt][c][3] += v.w;
+            for (int c = 0; c < 4; ++c) {
+              const float4 v = scr[(warp * 4 + c) * 32 + lane];
+              float* x = o[nt][c0 + c];
+              x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+            }
           }
         }
       }
-    }
-    if (warp == 0) {
-      const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      if (warp == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int h = 8 * nt + 2 * t + e;
           if (h >= G) continue;
           const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
-          const float inv = L[nt][e] == 0.f ? 0.f : 1.f / L[nt][e];
+          const float inv = L[e] == 0.f ? 0.f : 1.f / L[e];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float x = o[nt][c][e], y = o[nt][c][2 + e];
@@ -512,19 +569,20 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           }
           if (gq == 0) {
             if (!whole)
-              p.part_ml[slot * G + h] = make_float2(M[nt][e], L[nt][e]);
+              p.part_ml[slot * G + h] = make_float2(M[e], L[e]);
             else if (p.lse)
-              p.lse[head] = L[nt][e] == 0.f ? -INFINITY : (M[nt][e] + log2f(L[nt][e])) * 0.6931471805599453f;
+              p.lse[head] = L[e] == 0.f ? -INFINITY : (M[e] + log2f(L[e])) * 0.6931471805599453f;
           }
         }
+      }
     }
     bar();  // scratch and (m, l) may be written again
   };
 
   load_query();
   const int rbase = 16 * warp;
-  const int n_units = static_cast<int>(u1 - u0);
-  int64_t seg_first = u0 - cur.s;  // the segment's first unit (it may lie in an earlier run)
+  const int n_units = u1 - u0;
+  int seg_first = u0 - cur.s;  // the segment's first unit (it may lie in an earlier run)
   bool alive = true;  // false once a wait gave up: the barriers of a segment's end are still met
   for (int i = 0; i < n_units; ++i) {
     const uint32_t st = static_cast<uint32_t>(i) % T::NSTAGE;
@@ -540,37 +598,42 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[nt][e] = sd[nt][e] = 0.f;
-      if constexpr (kE4M3) {
+      {
         const int row = rbase + 8 * (mi & 1) + rr;
+        uint32_t b0, b1;
+        if constexpr (kE4M3) {
 #pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          uint32_t w0, w1, w2, w3;  // rows 0-7 and 8-15 of chunk c, then of chunk c + 1
-          ldmatrix_x4(kbase + sw128_off(row, c + (mi >> 1)), w0, w1, w2, w3);
-          const uint32_t a[4] = {f16x2_of_lo(w0), f16x2_of_lo(w1), f16x2_of_hi(w0), f16x2_of_hi(w1)};
-          const uint32_t b[4] = {f16x2_of_lo(w2), f16x2_of_lo(w3), f16x2_of_hi(w2), f16x2_of_hi(w3)};
+          for (int c = 0; c < 8; c += 2) {
+            uint32_t w0, w1, w2, w3;  // rows 0-7 and 8-15 of chunk c, then of chunk c + 1
+            ldmatrix_x4(kbase + sw128_off(row, c + (mi >> 1)), w0, w1, w2, w3);
+            const uint32_t a[4] = {f16x2_of_lo(w0), f16x2_of_lo(w1), f16x2_of_hi(w0), f16x2_of_hi(w1)};
+            const uint32_t b[4] = {f16x2_of_lo(w2), f16x2_of_lo(w3), f16x2_of_hi(w2), f16x2_of_hi(w3)};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(sc[nt], a, qb[0][nt][c][0], qb[0][nt][c][1]);
-            mma_f16_16816(sd[nt], b, qb[0][nt][c + 1][0], qb[0][nt][c + 1][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              q_frag(0, nt, c, b0, b1);
+              mma_f16_16816(sc[nt], a, b0, b1);
+              q_frag(0, nt, c + 1, b0, b1);
+              mma_f16_16816(sd[nt], b, b0, b1);
+            }
           }
-        }
-      } else {
-        const int row = rbase + 8 * (mi & 1) + rr;
+        } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int d8 = 2 * c + (mi >> 1);  // 16-byte chunk of 8 channels
-          uint32_t a0, a1, a2, a3;
-          ldmatrix_x4(kbase + (d8 >> 3) * T::HALF + sw128_off(row, d8 & 7), a0, a1, a2, a3);
+          for (int c = 0; c < 8; ++c) {
+            const int d8 = 2 * c + (mi >> 1);  // 16-byte chunk of 8 channels
+            uint32_t a0, a1, a2, a3;
+            ldmatrix_x4(kbase + (d8 >> 3) * T::HALF + sw128_off(row, d8 & 7), a0, a1, a2, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16_16816(sc[nt], a0, a1, a2, a3, qb[0][nt][c][0], qb[0][nt][c][1]);
-            mma_bf16_16816(sd[nt], a0, a1, a2, a3, qb[NQ - 1][nt][c][0], qb[NQ - 1][nt][c][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              q_frag(0, nt, c, b0, b1);
+              mma_bf16_16816(sc[nt], a0, a1, a2, a3, b0, b1);
+              q_frag(NQ - 1, nt, c, b0, b1);
+              mma_bf16_16816(sd[nt], a0, a1, a2, a3, b0, b1);
+            }
           }
         }
       }
       const bool in0 = rbase + gq < nvalid, in1 = rbase + 8 + gq < nvalid;
-      float lv = 0.f, iv = 1.f;
-      if constexpr (kE4M3) lv = meta.z, iv = meta.w;
+      const float lv = kE4M3 ? meta.z : 0.f, iv = kE4M3 ? meta.w : 1.f;
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -613,13 +676,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(sc[nt][e] - m[nt][e & 1]);
         l[nt][0] += (pr[0] + pr[2]) * iv;
         l[nt][1] += (pr[1] + pr[3]) * iv;
-        if constexpr (kE4M3) {
-          pb[nt][0] = movmatrix_trans(pack_f16x2(pr[0], pr[1]));
-          pb[nt][1] = movmatrix_trans(pack_f16x2(pr[2], pr[3]));
-        } else {
-          pb[nt][0] = movmatrix_trans(pack_bf16x2(pr[0], pr[1]));
-          pb[nt][1] = movmatrix_trans(pack_bf16x2(pr[2], pr[3]));
-        }
+        pb[nt][0] = movmatrix_trans(kE4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
+        pb[nt][1] = movmatrix_trans(kE4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
       }
       // value rows at or past len may hold anything (NaN included): zero them so
       // that P = 0 cannot meet NaN inside the product.
@@ -641,7 +699,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           uint32_t w[4];  // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
           ldmatrix_x4_trans(vbase + sw128_off(row, c + (mi >> 1)), w[0], w[1], w[2], w[3]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], 0u, 0x3120);  // even channels low, odd high
+          for (int k = 0; k < 4; ++k) w[k] = __byte_perm(w[k], 0u, 0x3120);  // even channels low, odd high
           const uint32_t a[4] = {f16x2_of_lo(w[0]), f16x2_of_hi(w[0]), f16x2_of_lo(w[1]), f16x2_of_hi(w[1])};
           const uint32_t b[4] = {f16x2_of_lo(w[2]), f16x2_of_hi(w[2]), f16x2_of_lo(w[3]), f16x2_of_hi(w[3])};
 #pragma unroll
@@ -676,63 +734,111 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       ++cur.s;
     }
   }
+  clear_empty<kSparse>(p, NCW * 32);
 }
 
-// One block per (sequence, query head), four warps: merges the partial results
-// of the runs that share it, in the order of the runs; a head written whole by
-// one run is left alone, a sequence without rows gets zeros.
-template <bool kSparse>
-__global__ void __launch_bounds__(128) decode_join_kernel(const Params p, int max_runs) {
-  const int64_t head = blockIdx.x;
-  const int b = static_cast<int>(head / p.Hq), hq = static_cast<int>(head % p.Hq);
-  const int g = hq / p.G, h = hq % p.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = p.lens[b];
-  if (hq == 0 && threadIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(p.max_blocks) * p.page_size))
-    raise_error(LLAMA_ATTN_DEVERR_CACHE_LEN);
-  const int64_t nst = stages_of<kSparse>(p, b);
-  if (nst == 0) {
-    p.out[head * 128 + threadIdx.x] = 0;
-    if (p.lse && threadIdx.x == 0) p.lse[head] = -INFINITY;
-    return;
-  }
-  const int64_t total = p.prefix[p.B], first = p.prefix[b] + g * nst;
-  const int64_t n_runs = min(static_cast<int64_t>(max_runs), total);
-  const int c0 = static_cast<int>(run_of(total, n_runs, first));
-  const int c1 = static_cast<int>(run_of(total, n_runs, first + nst - 1));
-  if (c0 == c1) return;
-  auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
-  __shared__ float s_m[4];
-  __shared__ float s_l[4];
-  __shared__ float4 s_o[4][32];
-  float M = -INFINITY;
-  for (int c = c0 + static_cast<int>(threadIdx.x); c <= c1; c += 128) M = fmaxf(M, p.part_ml[slot(c)].x);
+// Merges the partial results of the runs that share a (sequence, KV head), in
+// an order fixed by the runs. Heads that one run wrote whole and sequences
+// without rows are done already. Latency bounds it (a few dependent loads), so
+// there are two layouts; a pair spans several runs where there are fewer pairs
+// than runs:
+// kByRun = false: a block per query head, its eight warps share the pair's
+// partial rows (70B heads over one 9001-row sequence: 37 of them).
+// kByRun = true: a block per run, for the one pair that ends in it and began
+// before; a warp takes whole heads (64 sequences of 8 KV heads: 4096 blocks of
+// the first layout would find nothing to do in 9 of 10 cases).
+constexpr int JOIN_WARPS = 8;
+
+// One head's partial rows mine, mine + step .. c1 of c0 .. c1: their sum of
+// weights and rows relative to the greatest maximum M of all. The first rows
+// are on their way while M is found.
+template <typename Slot>
+__device__ __forceinline__ void join_rows(const Params& p, Slot slot, int c0, int c1, int mine, int step, float& M,
+                                          float& L, float4& acc) {
+  const int lane = threadIdx.x & 31;
+  float2 ml[4];
+  float4 v[4];
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + i * step <= c1) {
+        const int64_t s = slot(c + i * step);
+        ml[i] = p.part_ml[s];
+        v[i] = reinterpret_cast<const float4*>(p.part_o + s * 128)[lane];
+      }
+    }
+  };
+  fetch(mine);
+  M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[slot(c)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_m[warp] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const int64_t at = slot(c);
-    const float2 ml = p.part_ml[at];
-    const float4 v = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
-    const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - M);  // no row: zeros, or a NaN
-    L += w * ml.y;
-    acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = mine;;) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w = ml[i].x == -INFINITY ? 1.f : ex2_approx(ml[i].x - M);  // no row: zeros, or a NaN
+      L += w * ml[i].y;
+      acc.x += w * v[i].x, acc.y += w * v[i].y, acc.z += w * v[i].z, acc.w += w * v[i].w;
+    }
+    c += 4 * step;
+    if (c > c1) break;
+    fetch(c);
   }
-  s_o[warp][lane] = acc;
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  L = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  const float* so = reinterpret_cast<const float*>(s_o);
-  const int d = threadIdx.x;
-  const float x = (so[d] + so[128 + d]) + (so[256 + d] + so[384 + d]);
-  const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : x / L);
-  p.out[head * 128 + d] = *reinterpret_cast<const uint16_t*>(&y);
-  if (p.lse && d == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+template <bool kByRun>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Params p, int max_runs) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if constexpr (kByRun) {
+    const int4 end = p.ends[blockIdx.x];
+    if (end.x < 0) return;
+    const int c0 = end.z, c1 = blockIdx.x;
+    for (int h = warp; h < p.G; h += JOIN_WARPS) {
+      auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
+      float M, L;
+      float4 a;
+      join_rows(p, slot, c0, c1, c0, 1, M, L, a);
+      const int64_t head = static_cast<int64_t>(end.x) * p.Hq + end.y * p.G + h;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      *reinterpret_cast<uint2*>(p.out + head * 128 + 4 * lane) =
+          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+      if (p.lse && lane == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+  } else {
+    const int head = blockIdx.x, b = head / p.Hq, hq = head - b * p.Hq;
+    const int g = hq / p.G, h = hq - g * p.G;
+    __shared__ float s_l[JOIN_WARPS];
+    __shared__ float4 s_o[JOIN_WARPS][32];
+    const int total = p.prefix[p.B], first = p.prefix[b], end = p.prefix[b + 1];
+    if (end == first) return;
+    const Cut cut(total, min(max_runs, total));
+    const int nst = (end - first) / p.Hkv;
+    const int c0 = cut.run_of(first + g * nst), c1 = cut.run_of(first + (g + 1) * nst - 1);
+    if (c0 == c1) return;
+    auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
+    float M, L;
+    float4 acc;
+    join_rows(p, slot, c0, c1, c0 + warp, JOIN_WARPS, M, L, acc);
+    s_o[warp][lane] = acc;
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    if (threadIdx.x >= 128) return;
+    const float* so = reinterpret_cast<const float*>(s_o);
+    const int64_t at = static_cast<int64_t>(head) * 128 + threadIdx.x;
+    float x = 0.f;
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) x += so[128 * w + threadIdx.x], L += s_l[w];
+    const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : x / L);
+    p.out[at] = *reinterpret_cast<const uint16_t*>(&y);
+    if (p.lse && threadIdx.x == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
 }
 
 }  // namespace dpg

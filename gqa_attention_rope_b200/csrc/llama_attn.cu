@@ -260,12 +260,12 @@ int device_setup(int dev, int* n_sm) {
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<false>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<true>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::q8::qkv_fp8_rope_kernel), la::q8::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, false>), la::dpg::Tile<true>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, true>), la::dpg::Tile<true>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, false>), la::dpg::Tile<true>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, true>), la::dpg::Tile<true>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, false>), la::dpg::Tile<false>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, true>), la::dpg::Tile<false>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, false>), la::dpg::Tile<true, false>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, true>), la::dpg::Tile<true, true>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, false>), la::dpg::Tile<true, false>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, true>), la::dpg::Tile<true, true>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, false>), la::dpg::Tile<false, false>::SMEM_ALLOC);
+    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, true>), la::dpg::Tile<false, true>::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::pap::kv_append_paged_kernel<true, 256, 8>), 256 * 8 * 32);
     attr(reinterpret_cast<const void*>(la::sel::select_blocks_kernel), la::sel::MAX_BLOCKS * 8);
     int n = 0;
@@ -912,6 +912,40 @@ bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// theta_k = base^(-2k/128), kept for the last base this thread used.
+const la::RopeFreqs& rope_freqs(float base) {
+  thread_local la::RopeFreqs f;
+  thread_local float of = 0.f;
+  if (of != base) {
+    for (int k = 0; k < 64; ++k) f.theta[k] = std::pow(static_cast<double>(base), -2.0 * k / 128.0);
+    of = base;
+  }
+  return f;
+}
+
+// A launch that may begin while the kernel before it on the stream ends (the
+// kernel waits by itself before it touches global memory), in clusters of
+// `cluster` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             int cluster, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // The page pool's geometry and the kernels' index limits, before any launch.
 int check_pages(int B, int Hkv, int D, int page_size, int max_blocks, int n_pages) {
   if (B <= 0 || Hkv <= 0 || page_size <= 0 || max_blocks <= 0 || n_pages <= 0) return LLAMA_ATTN_ERR_INVALID_ARG;
@@ -989,26 +1023,26 @@ int kv_append_paged(const AppendArgs& a, cudaStream_t stream) {
   prof_count(1);
   const int pair = prof_before(stream);
   const int rows = a.T < a.page_size ? a.T : a.page_size;  // a CTA's rows at most
-  auto smem = [](int threads, int rows_per_thread) { return kE4M3 ? threads * rows_per_thread * 32 : 0; };
-  if (rows <= 16)
-    la::pap::kv_append_paged_kernel<kE4M3, 128, 2><<<grid, 128, smem(128, 2), stream>>>(p);
-  else if (rows <= 64)
-    la::pap::kv_append_paged_kernel<kE4M3, 128, 8><<<grid, 128, smem(128, 8), stream>>>(p);
-  else
-    la::pap::kv_append_paged_kernel<kE4M3, 256, 8><<<grid, 256, smem(256, 8), stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  auto launch = [&](void (*kernel)(la::pap::Params), int threads, int rows_per_thread) {
+    return launch_dependent(kernel, grid, threads, kE4M3 ? threads * rows_per_thread * 32 : 0, stream, 1, p);
+  };
+  const cudaError_t e = rows <= 16   ? launch(la::pap::kv_append_paged_kernel<kE4M3, 128, 2>, 128, 2)
+                        : rows <= 64 ? launch(la::pap::kv_append_paged_kernel<kE4M3, 128, 8>, 128, 8)
+                                     : launch(la::pap::kv_append_paged_kernel<kE4M3, 256, 8>, 256, 8);
   prof_after(pair, stream);
   return cuda_status(e);
 }
 
-// Workspace of decode_runs_kernel: units before each sequence, then (m, l)
-// and O of at most two partial results per run, each part 256-byte aligned.
+// Workspace of decode_runs_kernel: units before each sequence, the pair that
+// ends in each run, then (m, l) and O of at most two partial results per run,
+// each part 256-byte aligned.
 struct RunsWs {
-  size_t ml_off, o_off, total;
+  size_t ends_off, ml_off, o_off, total;
 };
 RunsWs runs_ws_layout(int64_t B, int64_t G) {
   RunsWs L;
-  L.ml_off = align256(static_cast<size_t>(B + 1) * sizeof(int64_t));
+  L.ends_off = align256(static_cast<size_t>(B + 1) * sizeof(int));
+  L.ml_off = L.ends_off + align256(static_cast<size_t>(la::dpg::MAX_CTAS) * sizeof(int4));
   L.o_off = L.ml_off + align256(static_cast<size_t>(2 * la::dpg::MAX_CTAS * G) * sizeof(float2));
   L.total = L.o_off + align256(static_cast<size_t>(2 * la::dpg::MAX_CTAS * G) * 128 * sizeof(float));
   return L;
@@ -1036,8 +1070,8 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   if (kSparse && a.n_sel <= 0) return LLAMA_ATTN_ERR_INVALID_ARG;
   if (a.q_pos_offset != 0 && a.q_pos_offset != -1) return LLAMA_ATTN_ERR_INVALID_ARG;
   if ((st = check_pages(a.B, a.Hkv, a.D, a.page_size, a.max_blocks, a.n_pages))) return st;
-  if (static_cast<int64_t>(a.B) * a.Hkv * a.max_blocks >= (int64_t(1) << 37) / (a.page_size / la::dpg::ROWS))
-    return LLAMA_ATTN_ERR_UNSUPPORTED;  // a run's units are counted in 32 bits
+  if (static_cast<int64_t>(a.B) * a.Hkv * a.max_blocks > INT32_MAX / (a.page_size / la::dpg::ROWS))
+    return LLAMA_ATTN_ERR_UNSUPPORTED;  // stages of all sequences and heads are counted in 32 bits
   const size_t rows_bytes = static_cast<size_t>(a.B) * a.Hq * 256;
   if (ranges_overlap(a.out, rows_bytes, a.q, rows_bytes)) return LLAMA_ATTN_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(a.lse) & 3u) return LLAMA_ATTN_ERR_INVALID_ARG;
@@ -1075,27 +1109,32 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   p.kscales = a.kscales;
   p.vscales = a.vscales;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
-  p.rope_theta = static_cast<double>(a.rope_theta);
+  p.freqs = rope_freqs(a.rope_theta);
   p.out = a.out;
   p.lse = a.lse;
-  p.prefix = reinterpret_cast<int64_t*>(ws);
+  p.prefix = reinterpret_cast<int*>(ws);
+  p.ends = reinterpret_cast<int4*>(ws + L.ends_off);
   p.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);
   p.epoch = next_epoch();
-  const int grid = 2 * n_sm < la::dpg::MAX_CTAS ? 2 * n_sm : la::dpg::MAX_CTAS;
-  constexpr uint32_t smem = la::dpg::Tile<kE4M3>::SMEM_ALLOC;
+  const int resident = n_sm * (G > 8 ? la::dpg::Tile<kE4M3, true>::CTAS : la::dpg::Tile<kE4M3, false>::CTAS);
+  const int grid = resident < la::dpg::MAX_CTAS ? resident : la::dpg::MAX_CTAS;
   std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
   prof_count(2);
   const int pair = prof_before(stream);
-  if (G > 8)
-    la::dpg::decode_runs_kernel<kE4M3, kSparse, true><<<grid, la::dpg::NTHREADS, smem, stream>>>(tk, tv, p);
-  else
-    la::dpg::decode_runs_kernel<kE4M3, kSparse, false><<<grid, la::dpg::NTHREADS, smem, stream>>>(tk, tv, p);
-  const cudaError_t e = cudaGetLastError();
+  using Wide = la::dpg::Tile<kE4M3, true>;
+  using Narrow = la::dpg::Tile<kE4M3, false>;
+  const cudaError_t e =
+      G > 8 ? launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, true>, dim3(grid), Wide::NTHREADS,
+                               Wide::SMEM_ALLOC, stream, 1, tk, tv, p)
+            : launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, false>, dim3(grid), Narrow::NTHREADS,
+                               Narrow::SMEM_ALLOC, stream, 1, tk, tv, p);
   prof_after(pair, stream);
   if (e != cudaSuccess) return LLAMA_ATTN_ERR_CUDA;
-  la::dpg::decode_join_kernel<kSparse><<<a.B * a.Hq, 128, 0, stream>>>(p, grid);
-  return cuda_status(cudaGetLastError());
+  const bool by_run = static_cast<int64_t>(a.B) * a.Hkv > grid;
+  return cuda_status(launch_dependent(by_run ? la::dpg::decode_join_kernel<true> : la::dpg::decode_join_kernel<false>,
+                                      dim3(by_run ? grid : a.B * a.Hq), la::dpg::JOIN_WARPS * 32, 0, stream, 1, p,
+                                      grid));
 }
 
 }  // namespace
@@ -1201,29 +1240,18 @@ int llama_attn_select_blocks(const llama_attn_bf16* q, const llama_attn_bf16* kb
   p.n_first = n_first;
   p.n_last = n_last;
   p.q_pos_offset = q_pos_offset;
-  p.rope_theta = static_cast<double>(rope_theta);
-  // Clusters widen while the GPU has room for another CTA per pair and each
-  // would still have one pass (16 warps x 8 blocks) of its own.
+  p.freqs = rope_freqs(rope_theta);
+  // Clusters widen while every CTA stays resident (four per SM) and has at
+  // least one pass (8 warps x 16 blocks) of its own.
   const int64_t groups = static_cast<int64_t>(B) * Hkv;
   int csize = 1;
-  while (csize < 8 && groups * csize * 2 <= 2 * n_sm && max_blocks > csize * la::sel::NWARPS * 8) csize *= 2;
+  while (csize < 8 && groups * csize * 2 <= 8 * n_sm && max_blocks > csize * la::sel::NWARPS * 16) csize *= 2;
   if (groups * csize > INT32_MAX) return LLAMA_ATTN_ERR_UNSUPPORTED;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = csize;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(groups * csize));
-  cfg.blockDim = dim3(la::sel::NTHREADS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(max_blocks) * 8;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
   prof_count(1);
   const int pair = prof_before(stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, la::sel::select_blocks_kernel, p);
+  const cudaError_t e = launch_dependent(la::sel::select_blocks_kernel, dim3(static_cast<unsigned>(groups * csize)),
+                                         la::sel::NTHREADS, static_cast<size_t>(max_blocks) * 8, stream, csize, p);
   prof_after(pair, stream);
   return cuda_status(e);
 }

@@ -391,6 +391,8 @@ template <bool kE4M3, int kThreads, int kRows>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 6) kv_append_paged_kernel(const Params p) {
   __shared__ float s_amax[kThreads / 32];
   __shared__ __align__(16) float s_bound[kThreads / 32][2][128];
+  grid_launch_dependents();
+  grid_dependency_wait();
   const Job j = job_of(p, blockIdx.z, blockIdx.y, blockIdx.x >> 1, blockIdx.x == 0 && blockIdx.y == 0);
   if (j.n <= 0) return;
   if (blockIdx.x & 1)

@@ -29,6 +29,12 @@ __global__ void rope_table_kernel(float2* __restrict__ tab, int maxpos, int D, d
   }
 }
 
+// theta_k of a head of 128 in float64, formed on the host and passed by value:
+// a kernel that turns a single row forms the angle from it without a pow.
+struct RopeFreqs {
+  double theta[64];
+};
+
 // Document layout from doc_offsets (cumulative starts in flattened B*S
 // coordinates, ending with the sentinel B*S; the count is implicit, so an
 // entry may only be read once every earlier one is known to be below B*S).

@@ -487,8 +487,8 @@ int llama_attn_decode_paged_e4m3(const llama_attn_bf16 *q, const uint8_t *kpages
  *   max_blocks <= 24576 (else LLAMA_ATTN_ERR_UNSUPPORTED).
  * A page id outside [0, n_pages) sets LLAMA_ATTN_DEVERR_BLOCK_TABLE and its
  * block scores 0; a length outside [0, max_blocks * page_size] sets
- * LLAMA_ATTN_DEVERR_CACHE_LEN and the ids are -1. A NaN score counts as the
- * greatest.
+ * LLAMA_ATTN_DEVERR_CACHE_LEN and the ids are -1. Where q or kbounds are not
+ * finite, which blocks are chosen is unspecified (n_sel of them all the same).
  */
 int llama_attn_select_blocks(const llama_attn_bf16 *q, const llama_attn_bf16 *kbounds,
                              const int32_t *block_table, const int32_t *cache_lens, int32_t *block_ids,

@@ -442,6 +442,47 @@ def test_select_ties_and_equal_scores():
         assert ids[0, 0].tolist() == sorted([0, 1] + best + [nb - 1])
 
 
+@pytest.mark.parametrize("spread", [0, 1])
+def test_select_decides_near_scores_in_float64(spread):
+    """Blocks whose scores differ by 1e-9 of their size and less: the order is float64's, which the
+    reference forms as a sum over heads of maxima."""
+    Hq, Hkv, page, nb, n_sel = 8, 2, 64, 700, 40
+    g = gen(5)
+    q = torch.randn(1, Hq, D, generator=g).to(torch.bfloat16)
+    base = torch.randn(Hkv, 2, D, generator=g).sort(dim=1).values.mul(4).to(torch.bfloat16)
+    bounds = base.expand(nb, -1, -1, -1).clone()
+    bounds[:, :, :, 17] = (torch.randn(nb, Hkv, 2, generator=g).abs() * 2.0 ** -24).to(torch.bfloat16)
+    bounds[:, :, 0, 17] *= -1
+    if spread:  # and as many far from them on both sides
+        bounds[::3] = (bounds[::3].float() * 0.5).to(torch.bfloat16)
+        bounds[1::40] = (bounds[1::40].float() * 1.5).to(torch.bfloat16)
+    table = torch.randperm(nb, generator=g).to(torch.int32)[None]
+    lens = [nb * page - 5]
+    ids = la.llama_attn_select_blocks(q.cuda(), bounds.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                      page, n_sel)
+    assert torch.equal(ids.cpu(), R.select(q, bounds, table, lens, page, n_sel, 1, 1, THETA))
+
+
+def test_select_with_values_that_are_not_finite_gives_distinct_ascending_ids():
+    nb, page = 500, 64
+    g = gen(6)
+    table = torch.randperm(nb, generator=g).to(torch.int32)[None].cuda()
+    lens = torch.tensor([nb * page], dtype=torch.int32, device="cuda")
+    for bad in (math.nan, math.inf, -math.inf, 3.3e38):
+        for every in (1, 3, 500):
+            bounds = torch.randn(nb, 1, 2, D, generator=g).sort(dim=2).values.to(torch.bfloat16)
+            bounds[::every, 0, 0, 5] = bad
+            q = torch.randn(1, 4, D, generator=g).to(torch.bfloat16)
+            for qq in (q, q * 1e30, torch.full_like(q, bad)):
+                for n_sel in (3, 300):
+                    buf, ids = guarded((1, 1, n_sel), torch.int32, 12345)
+                    la.llama_attn_select_blocks(qq.cuda(), bounds.cuda(), table, lens, page, n_sel, block_ids=ids)
+                    torch.cuda.synchronize()
+                    check_guard(buf, 12345, "block_ids")
+                    i = ids[0, 0].tolist()
+                    assert i[0] == 0 and i[-1] == nb - 1 and all(a < b for a, b in zip(i, i[1:]))
+
+
 @pytest.mark.parametrize("B,Hkv,nb", [(1, 1, 2048), (1, 8, 1000), (40, 8, 129), (2, 2, 24576)])
 def test_select_cluster_sizes(B, Hkv, nb):
     """Every cluster width, up to the greatest number of blocks."""
