@@ -1131,7 +1131,9 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
                                Narrow::SMEM_ALLOC, stream, 1, tk, tv, p);
   prof_after(pair, stream);
   if (e != cudaSuccess) return LLAMA_ATTN_ERR_CUDA;
-  const bool by_run = static_cast<int64_t>(a.B) * a.Hkv > grid;
+  // a pair spans grid / (B * Hkv) runs on average: from 8 on its partial rows
+  // are enough for the eight warps of a block
+  const bool by_run = static_cast<int64_t>(a.B) * a.Hkv * 8 > grid;
   return cuda_status(launch_dependent(by_run ? la::dpg::decode_join_kernel<true> : la::dpg::decode_join_kernel<false>,
                                       dim3(by_run ? grid : a.B * a.Hq), la::dpg::JOIN_WARPS * 32, 0, stream, 1, p,
                                       grid));
@@ -1242,10 +1244,10 @@ int llama_attn_select_blocks(const llama_attn_bf16* q, const llama_attn_bf16* kb
   p.q_pos_offset = q_pos_offset;
   p.freqs = rope_freqs(rope_theta);
   // Clusters widen while every CTA stays resident (four per SM) and has at
-  // least one pass (8 warps x 16 blocks) of its own.
+  // least one pass (8 warps x 8 blocks) of its own.
   const int64_t groups = static_cast<int64_t>(B) * Hkv;
   int csize = 1;
-  while (csize < 8 && groups * csize * 2 <= 8 * n_sm && max_blocks > csize * la::sel::NWARPS * 16) csize *= 2;
+  while (csize < 8 && groups * csize * 2 <= 4 * n_sm && max_blocks > csize * la::sel::NWARPS * 8) csize *= 2;
   if (groups * csize > INT32_MAX) return LLAMA_ATTN_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
   prof_count(1);

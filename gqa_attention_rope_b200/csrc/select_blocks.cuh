@@ -13,20 +13,15 @@
 // than the first n_first and the last n_last blocks those with the greatest
 // scores are taken, of equal scores the lower index.
 //
-// Most blocks are far from the border, so the scores are first formed on the
-// tensor cores: 16 blocks are the rows of an m16n8k16 product over the 256
-// bounds, and three of its 8 columns carry the weights as three bf16 terms (24
-// bits), which costs nothing next to one. Products of bf16 are exact; the 16
-// accumulations in float32 and the residue of the weights stay within
-// eps = 2^-15 sum_d |w_d| max |bound| (were each of a product's 17 terms cut
-// off at 2^-23 of that sum, 16 products would reach 2^-15). A radix selection
-// over these scores finds a range [lo, hi] that holds the one at the border;
-// blocks outside [lo - 2 eps, hi + 2 eps] are decided by it, the one or two
-// inside get their float64 score and a second selection.
-// Measured for 64 sequences of 1024 to 32768 rows (8 KV heads, 64-row blocks,
-// 71 MB of bounds): all scores in float64 39 us, three quarters of it
-// instructions (400 per warp and 8 blocks); this form: see the table of
-// results beside the kernel's launch.
+// Most blocks are far from the border, so the scores are first formed in
+// float32: a weight's rounding, 8 products and sums per lane and 5 sums over
+// the lanes stay within eps = 2^-20 sum_d |w_d| max |bound| (14 roundings of
+// 2^-24). A radix selection over these scores finds a range [lo, hi] that holds
+// the one at the border; blocks outside [lo - 2 eps, hi + 2 eps] are decided by
+// it, and the few inside get their float64 score and are ranked by it.
+// With all scores in float64 the 64 sequences below took 39 us; on the tensor
+// cores (three bf16 terms of the weights as columns of one product) the sums
+// were cheaper but bound only to 2^-15, which left several blocks near.
 //
 // One cluster of CTAs takes one (sequence, KV head): each CTA streams its
 // share of the bounds and stores an order-preserving key of every score into
@@ -197,16 +192,21 @@ __device__ __forceinline__ void radix_select(RadixShared& s, Key key, int c0, in
   }
 }
 
+constexpr int kNearCap = 64;  // near blocks that are ranked pair by pair
+
 // grid (cluster size * B * Hkv): consecutive CTAs form the cluster of one
 // (sequence, KV head). Dynamic shared memory: 8 bytes per block of a sequence.
 __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params p) {
-  extern __shared__ unsigned long long s_key[];    // first the scores' 32-bit keys, then kIn, kOut or a float64's key
-  __shared__ __align__(16) double s_w[256];        // weights of the minima (down), then of the maxima (up)
-  __shared__ uint2 s_b[16][32];                    // the same as fragments of the product, three bf16 terms
+  extern __shared__ unsigned long long s_key[];  // the scores' 32-bit keys, then (many near blocks) kIn, kOut or a float64's key
+  __shared__ __align__(16) double s_w[256];      // weights of the minima (down), then of the maxima (up)
   __shared__ RadixShared s_radix;
-  __shared__ uint32_t s_mag[8 * NWARPS];           // per warp of the cluster: greatest magnitude of a bound, float bits
-  __shared__ double s_wsum[4];
-  __shared__ int s_count[2][NWARPS];
+  __shared__ uint32_t s_mag[8 * NWARPS];         // per warp of the cluster: greatest magnitude of a bound, float bits
+  __shared__ double s_wsum[2];
+  __shared__ uint32_t s_in[MAX_BLOCKS / 32], s_eq[MAX_BLOCKS / 32];  // a bit per block: chosen; one of the first `take` of these
+  __shared__ int s_near[kNearCap];
+  __shared__ unsigned long long s_near_key[kNearCap];
+  __shared__ int s_n_in, s_n_near;
+  __shared__ int s_scan[2][NWARPS];
 
   const uint32_t rank = cluster_rank(), csize = cluster_size();
   const int64_t bg = blockIdx.x / csize;
@@ -226,6 +226,29 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
       for (int i = threadIdx.x; i < p.n_sel; i += NTHREADS) ids[i] = i < nb ? i : -1;
     return;
   }
+  const int c0 = p.n_first, c1 = nb - p.n_last;  // candidates [c0, c1); more than n_sel - n_first - n_last of them
+  const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+  const int step = static_cast<int>(csize) * NWARPS * 8;
+  const int j_first = c0 + (static_cast<int>(rank) * NWARPS + warp) * 8;
+  auto page_at = [&](int j0) { return lane < 8 && j0 + lane < c1 ? table[j0 + lane] : 0; };
+  int page = page_at(j_first);
+  uint4 u[2][4];  // bounds of 8 blocks: lanes 0-15 minima of channels 8 * lane.., lanes 16-31 maxima
+  auto fetch = [&](int half, int pages, int j0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, pages, 4 * half + i);
+      u[half][i] = make_uint4(0u, 0u, 0u, 0u);  // a block that is not there scores as zeros
+      if (j0 + 4 * half + i < c1) {
+        if (pg >= 0 && pg < p.n_pages)
+          u[half][i] = __ldg(reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pg) * p.Hkv + g) * 256) + lane);
+        else if (lane == 0)
+          raise_error(LLAMA_ATTN_DEVERR_BLOCK_TABLE);
+      }
+    }
+  };
+  fetch(0, page, j_first);
+  fetch(1, page, j_first);
+  page = page_at(j_first + step);
 
   // ---- the group's weights: up_d, down_d of the query rotated at its position
   if (threadIdx.x < 64) {
@@ -236,8 +259,8 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
     const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q + (static_cast<int64_t>(b) * p.Hq + g * p.G) * 128) + k;
 #pragma unroll 4
     for (int h = 0; h < p.G; ++h) {
-      const uint32_t u = q[h * 64];
-      const double x0 = bf16_lo(u), x1 = bf16_hi(u);
+      const uint32_t x = q[h * 64];
+      const double x0 = bf16_lo(x), x1 = bf16_hi(x);
       const double y0 = x0 * cs - x1 * sn, y1 = x0 * sn + x1 * cs;
       w[0] += fmin(y0, 0.0), w[1] += fmin(y1, 0.0), w[2] += fmax(y0, 0.0), w[3] += fmax(y1, 0.0);
     }
@@ -247,80 +270,61 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_wsum[warp] = sum;
   }
-  __syncthreads();
-  // Fragments: a thread (row group gq, t) of the product loads 8 neighbouring
-  // bounds 32 i + 8 t.. of a block, which are its part of steps 2 i and 2 i + 1.
-  for (int e = threadIdx.x; e < 16 * 32; e += NTHREADS) {
-    const int st = e >> 5, gq = (e & 31) >> 2, t = e & 3;
-    const double* w = s_w + 32 * (st >> 1) + 8 * t + 4 * (st & 1);
-    uint32_t r[2] = {0u, 0u};
-    if (gq < 3) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        double rest = w[i];
-        __nv_bfloat16 term = __float2bfloat16_rn(0.f);
-        for (int n = 0; n <= gq; ++n) {
-          term = __float2bfloat16_rn(static_cast<float>(rest));
-          rest -= static_cast<double>(__bfloat162float(term));
-        }
-        r[i >> 1] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&term)) << (16 * (i & 1));
-      }
-    }
-    s_b[st][e & 31] = make_uint2(r[0], r[1]);
-  }
-  __syncthreads();
+  if (threadIdx.x == 64) s_n_in = s_n_near = 0;
   // every CTA of the cluster has started before any of them stores into the first one
-  if (csize > 1) cluster_sync();
+  if (csize > 1)
+    cluster_sync();
+  else
+    __syncthreads();
 
-  // ---- scores, 16 candidates at a time per warp
-  const int c0 = p.n_first, c1 = nb - p.n_last;  // candidates [c0, c1); more than n_sel - n_first - n_last of them
-  const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+  // ---- scores, 8 candidates at a time per warp, the next ones' bounds on their way
+  const double* lane_w = s_w + 8 * lane;
   {
-    const int gq = lane >> 2, t = lane & 3;
-    const int step = static_cast<int>(csize) * NWARPS * 16;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = static_cast<float>(lane_w[i]);
     uint32_t mag = 0u;
-    int j0 = c0 + (static_cast<int>(rank) * NWARPS + warp) * 16;
-    int next = lane < 16 && j0 + lane < c1 ? table[j0 + lane] : 0;
-    for (; j0 < c1; j0 += step) {
-      int page = next;
-      next = lane < 16 && j0 + step + lane < c1 ? table[j0 + step + lane] : 0;
-      if (page < 0 || page >= p.n_pages) {
-        raise_error(LLAMA_ATTN_DEVERR_BLOCK_TABLE);
-        page = -1;
-      }
-      const int pa = __shfl_sync(0xffffffffu, page, gq), pb = __shfl_sync(0xffffffffu, page, gq + 8);
-      const bool ina = j0 + gq < c1 && pa >= 0, inb = j0 + gq + 8 < c1 && pb >= 0;  // others score as zeros
-      const uint4* xa = reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pa) * p.Hkv + g) * 256) + t;
-      const uint4* xb = reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pb) * p.Hkv + g) * 256) + t;
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = j_first; j0 < c1; j0 += step) {
+      const int page2 = page_at(j0 + 2 * step);
+      float v[8];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint4 a[4], c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a[i] = c[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (ina) a[i] = __ldg(xa + 4 * (4 * half + i));
-          if (inb) c[i] = __ldg(xb + 4 * (4 * half + i));
+          const uint4 x = u[half][i];
+          const float2 a = unpack_bf16x2(x.x), e = unpack_bf16x2(x.y), f = unpack_bf16x2(x.z), h = unpack_bf16x2(x.w);
+          float y = w[0] * a.x;
+          y = fmaf(w[1], a.y, y);
+          y = fmaf(w[2], e.x, y);
+          y = fmaf(w[3], e.y, y);
+          y = fmaf(w[4], f.x, y);
+          y = fmaf(w[5], f.y, y);
+          y = fmaf(w[6], h.x, y);
+          v[4 * half + i] = fmaf(w[7], h.y, y);
+          mag = max_abs(mag, max_abs(max_abs(x.x, x.y), max_abs(x.z, x.w)));
         }
+        fetch(half, page, j0 + step);
+      }
+      page = page2;
+      // Sum each of the 8 over the 32 lanes: three steps that halve the number
+      // of sums a lane carries, then two plain ones.
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint2 w0 = s_b[2 * (4 * half + i)][lane], w1 = s_b[2 * (4 * half + i) + 1][lane];
-          mma_bf16_16816(s0, a[i].x, c[i].x, a[i].y, c[i].y, w0.x, w0.y);
-          mma_bf16_16816(s1, a[i].z, c[i].z, a[i].w, c[i].w, w1.x, w1.y);
-          mag = max_abs(max_abs(max_abs(mag, a[i].x), max_abs(a[i].y, a[i].z)),
-                        max_abs(max_abs(a[i].w, c[i].x), max_abs(max_abs(c[i].y, c[i].z), c[i].w)));
+      for (int s = 0; s < 3; ++s) {
+        const int bit = 16 >> s, n = 4 >> s;
+        const bool upper = lane & bit;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float send = upper ? v[i] : v[i + n], mine = upper ? v[i + n] : v[i];
+          v[i] = mine + __shfl_xor_sync(0xffffffffu, send, bit);
         }
       }
-      // columns 0 and 1 of rows gq and gq + 8 are in lane t = 0, column 2 in lane t = 1
-      float u = s0[0] + s1[0], v = s0[2] + s1[2];
-      u += __shfl_down_sync(0xffffffffu, u, 1) + (s0[1] + s1[1]);
-      v += __shfl_down_sync(0xffffffffu, v, 1) + (s0[3] + s1[3]);
-      if (t == 0) {
-        if (j0 + gq < c1) store_to_first32(smem_addr(s_key + j0 + gq), order_key(u));
-        if (j0 + gq + 8 < c1) store_to_first32(smem_addr(s_key + j0 + gq + 8), order_key(v));
-      }
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+      const int j = j0 + (lane >> 2);  // lane bits 4, 3, 2 = candidate bits 2, 1, 0
+      if ((lane & 3) == 0 && j < c1) store_to_first32(smem_addr(s_key + j), order_key(v[0]));
     }
-    mag = __reduce_max_sync(0xffffffffu, max((mag << 16) & 0x7FFF0000u, mag & 0x7FFF0000u));  // magnitudes order like their bits
+    // magnitudes order like their bits
+    mag = __reduce_max_sync(0xffffffffu, max((mag << 16) & 0x7FFF0000u, mag & 0x7FFF0000u));
     if (lane == 0) store_to_first32(smem_addr(&s_mag[rank * NWARPS + warp]), mag);
   }
   if (csize > 1)
@@ -332,94 +336,137 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
   // ---- the first CTA: which candidates the scores decide
   const int need = p.n_sel - p.n_first - p.n_last;
   auto approx = [&](int j) { return static_cast<uint32_t>(s_key[j]); };
-  int n_in = 0, n_near = 0;
+  float lo = INFINITY, hi = INFINITY;  // need == 0: no candidate reaches lo
   if (need > 0) {
-    uint32_t mag = 0u;
-    for (int i = 0; i < static_cast<int>(csize) * NWARPS; ++i) mag = max(mag, s_mag[i]);
-    const float eps2 = 2.f * 0x1p-15f * static_cast<float>(s_wsum[0] + s_wsum[1]) * __uint_as_float(mag);
+    uint32_t mag = lane < static_cast<int>(csize) * NWARPS ? s_mag[lane] : 0u;
+    if (lane + 32 < static_cast<int>(csize) * NWARPS) mag = max(mag, s_mag[lane + 32]);
+    mag = __reduce_max_sync(0xffffffffu, mag);
+    const float eps2 = 2.f * 0x1p-20f * static_cast<float>(s_wsum[0] + s_wsum[1]) * __uint_as_float(mag);
     uint32_t klo, khi;
     int unused;
     radix_select<false>(s_radix, approx, c0, c1, need, klo, khi, unused);
-    const float lo = score_of(klo) - eps2, hi = score_of(khi) + eps2;
-    const int group = lane >> 4, ch = lane & 15;
-    for (int j0 = c0 + warp * 32; j0 < c1; j0 += NTHREADS) {
-      const int j = j0 + lane;
-      const float s = j < c1 ? score_of(approx(j)) : 0.f;
-      const bool in = j < c1 && s > hi, out = j < c1 && s < lo;  // a NaN is neither
-      if (in || out) s_key[j] = in ? kIn : kOut;
-      n_in += __popc(__ballot_sync(0xffffffffu, in));
-      unsigned near = __ballot_sync(0xffffffffu, j < c1 && !in && !out);
-      n_near += __popc(near);
-      for (; near; near &= near - 1) {  // float64, the whole warp
-        const int n = j0 + __ffs(near) - 1;
-        const int page = table[n];
-        double x = 0.0;
-        if (page >= 0 && page < p.n_pages) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(page) * p.Hkv + g) * 256) + lane);
-          const double* w = s_w + 128 * group + 8 * ch;
-          x = w[0] * bf16_lo(u.x);
-          x = fma(w[1], bf16_hi(u.x), x);
-          x = fma(w[2], bf16_lo(u.y), x);
-          x = fma(w[3], bf16_hi(u.y), x);
-          x = fma(w[4], bf16_lo(u.z), x);
-          x = fma(w[5], bf16_hi(u.z), x);
-          x = fma(w[6], bf16_lo(u.w), x);
-          x = fma(w[7], bf16_hi(u.w), x);
-        }
-        // the same tree for every block, so equal bounds give equal scores
+    lo = score_of(klo) - eps2;
+    hi = score_of(khi) + eps2;
+  }
+  // 2: chosen, 1: near, 0: not chosen. A NaN is near, whatever else it is.
+  auto decide = [&](int j) {
+    if (j < c0 || j >= c1) return 2;
+    if (need == 0) return 0;
+    const float x = score_of(approx(j));
+    return x > hi ? 2 : x < lo ? 0 : 1;
+  };
+  const int nb32 = (nb + 31) & ~31;
+  for (int j0 = warp * 32; j0 < nb32; j0 += NTHREADS) {
+    const int j = j0 + lane, d = j < nb ? decide(j) : 0;
+    const unsigned in = __ballot_sync(0xffffffffu, d == 2), near = __ballot_sync(0xffffffffu, d == 1);
+    if (lane == 0) {
+      s_in[j0 >> 5] = in;
+      s_eq[j0 >> 5] = 0u;
+      if (in) atomicAdd(&s_n_in, __popc(in));
+    }
+    if (near) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_n_near, __popc(near));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(near & ((1u << lane) - 1u));
+      if (d == 1 && at < kNearCap) s_near[at] = j;
+    }
+  }
+  __syncthreads();
+  const int n_near = s_n_near;
+  int take = p.n_sel - s_n_in;  // of the near ones
+  // float64 score of block j, by a whole warp; the same tree for every block,
+  // so equal bounds give equal scores
+  auto exact = [&](int j) {
+    const int pg = table[j];
+    double x = 0.0;
+    if (pg >= 0 && pg < p.n_pages) {
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pg) * p.Hkv + g) * 256) + lane);
+      x = lane_w[0] * bf16_lo(y.x);
+      x = fma(lane_w[1], bf16_hi(y.x), x);
+      x = fma(lane_w[2], bf16_lo(y.y), x);
+      x = fma(lane_w[3], bf16_hi(y.y), x);
+      x = fma(lane_w[4], bf16_lo(y.z), x);
+      x = fma(lane_w[5], bf16_hi(y.z), x);
+      x = fma(lane_w[6], bf16_lo(y.w), x);
+      x = fma(lane_w[7], bf16_hi(y.w), x);
+    }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) s_key[n] = order_key(x);
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return order_key(x);
+  };
+  if (n_near <= kNearCap) {
+    if (take < n_near) {
+      for (int i = warp; i < n_near; i += NWARPS) {
+        const unsigned long long k = exact(s_near[i]);
+        if (lane == 0) s_near_key[i] = k;
       }
+      __syncthreads();
+    }
+    if (static_cast<int>(threadIdx.x) < n_near) {
+      const int j = s_near[threadIdx.x];
+      int above = 0;  // near blocks that come before this one
+      if (take < n_near) {
+        const unsigned long long k = s_near_key[threadIdx.x];
+        for (int i = 0; i < n_near; ++i) above += s_near_key[i] > k || (s_near_key[i] == k && s_near[i] < j) ? 1 : 0;
+      }
+      if (above < take) atomicOr(&s_in[j >> 5], 1u << (j & 31));
     }
   } else {
-    for (int j = c0 + threadIdx.x; j < c1; j += NTHREADS) s_key[j] = kOut;
+    // many near blocks (equal or nearly equal bounds): all their float64 scores, and a second selection
+    for (int j0 = c0 + warp * 32; j0 < c1; j0 += NTHREADS) {
+      const int j = j0 + lane, d = j < c1 ? decide(j) : 0;
+      __syncwarp();
+      if (j < c1 && d != 1) s_key[j] = d == 2 ? kIn : kOut;
+      for (unsigned near = __ballot_sync(0xffffffffu, d == 1); near; near &= near - 1) {
+        const int n = j0 + __ffs(near) - 1;
+        const unsigned long long k = exact(n);
+        if (lane == 0) s_key[n] = k;
+      }
+    }
+    __syncthreads();
+    unsigned long long klo = 1ull, khi = 1ull;
+    const bool all = take >= n_near;
+    if (!all) radix_select<true>(s_radix, [&](int j) { return s_key[j]; }, c0, c1, take, klo, khi, take);
+    for (int j0 = warp * 32; j0 < nb32; j0 += NTHREADS) {
+      const int j = j0 + lane;
+      const unsigned long long k = j >= c0 && j < c1 ? s_key[j] : kOut;
+      const bool near = k != kIn && k != kOut;
+      const unsigned in = __ballot_sync(0xffffffffu, near && (all || k > khi));
+      const unsigned eq = __ballot_sync(0xffffffffu, near && !all && k >= klo && k <= khi);
+      if (lane == 0) s_in[j0 >> 5] |= in, s_eq[j0 >> 5] = eq;
+    }
   }
-  if (lane == 0) s_count[0][warp] = n_in, s_count[1][warp] = n_near;
+  if (n_near <= kNearCap) take = 0;  // nothing is in s_eq
   __syncthreads();
-  n_in = n_near = 0;
-#pragma unroll
-  for (int i = 0; i < NWARPS; ++i) n_in += s_count[0][i], n_near += s_count[1][i];
 
-  // ---- of the near ones the `take` greatest by float64: those above hi, and of [lo, hi] the first `take`
-  unsigned long long lo = 1ull, hi = 1ull;
-  int take = need - n_in;
-  const bool all = take >= n_near;
-  if (!all) {
-    auto exact = [&](int j) { return s_key[j]; };
-    radix_select<true>(s_radix, exact, c0, c1, take, lo, hi, take);
-  }
-  // ---- the chosen ids in ascending order: each warp a stretch of the blocks
-  const int span = ((nb + NWARPS - 1) / NWARPS + 31) / 32 * 32;
-  const int w0 = min(nb, warp * span), w1 = min(nb, w0 + span);
-  auto state = [&](int j) {  // 2: chosen, 1: in the range, 0: not
-    if (j >= w1) return 0;
-    if (j < c0 || j >= c1) return 2;
-    const unsigned long long k = s_key[j];
-    if (k == kOut) return 0;
-    return all || k > hi ? 2 : k >= lo ? 1 : 0;
-  };
-  auto before = [&](unsigned ball) { return __popc(ball & ((1u << lane) - 1u)); };
-  int n_sure = 0, n_eq = 0;
-  for (int j = w0; j < w1; j += 32) {
-    const int s = state(j + lane);
-    n_sure += __popc(__ballot_sync(0xffffffffu, s == 2));
-    n_eq += __popc(__ballot_sync(0xffffffffu, s == 1));
-  }
-  __syncthreads();
-  if (lane == 0) s_count[0][warp] = n_sure, s_count[1][warp] = n_eq;
-  __syncthreads();
-  int sure = 0, eq = 0;
+  // ---- the chosen ids in ascending order: a thread has a stretch of words
+  const int words = nb32 >> 5, per = (words + NTHREADS - 1) / NTHREADS;
+  const int w0 = min(words, static_cast<int>(threadIdx.x) * per), w1 = min(words, w0 + per);
+  int n_in = 0, n_eq = 0;
+  for (int w = w0; w < w1; ++w) n_in += __popc(s_in[w]), n_eq += __popc(s_eq[w]);
+  int in_before = n_in, eq_before = n_eq;
 #pragma unroll
-  for (int i = 0; i < NWARPS; ++i) sure += i < warp ? s_count[0][i] : 0, eq += i < warp ? s_count[1][i] : 0;
-  for (int j = w0; j < w1; j += 32) {
-    const int s = state(j + lane);
-    const unsigned bs = __ballot_sync(0xffffffffu, s == 2), be = __ballot_sync(0xffffffffu, s == 1);
-    const int eq_before = eq + before(be);
-    const int at = sure + before(bs) + min(eq_before, take);
-    if (s == 2 || (s == 1 && eq_before < take)) ids[at] = j + lane;
-    sure += __popc(bs);
-    eq += __popc(be);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, in_before, o), y = __shfl_up_sync(0xffffffffu, eq_before, o);
+    if (lane >= o) in_before += x, eq_before += y;
+  }
+  if (lane == 31) s_scan[0][warp] = in_before, s_scan[1][warp] = eq_before;
+  __syncthreads();
+  in_before -= n_in;
+  eq_before -= n_eq;
+  for (int i = 0; i < warp; ++i) in_before += s_scan[0][i], eq_before += s_scan[1][i];
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t in = s_in[w], eq = s_eq[w];
+    for (uint32_t rest = in | eq; rest; rest &= rest - 1) {
+      const int bit = __ffs(rest) - 1;
+      if (in >> bit & 1) {
+        ids[in_before + min(eq_before, take)] = 32 * w + bit;
+        ++in_before;
+      } else {
+        if (eq_before < take) ids[in_before + eq_before] = 32 * w + bit;
+        ++eq_before;
+      }
+    }
   }
 }
 
