@@ -390,7 +390,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
   const int gq = lane >> 2, t = lane & 3;
   const int G = p.G;
   auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory"); };
-  uint32_t qb[T::Q_REGS ? NQ : 1][T::Q_REGS ? NT : 1][8][2];
+  uint32_t qb[T::Q_REGS ? NQ : 1][T::Q_REGS ? NT : 1][8][2] = {};
   float qf[NT][2], m[NT][2], l[NT][2];
   float o[NT][8][4];
   // B fragment of the query for k step c, from shared memory; q_frag: from where the kernel keeps it.
@@ -593,11 +593,15 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     if (alive && rbase < nvalid) {
       const uint32_t kbase = sbase + st * T::STAGE, vbase = kbase + T::TENSOR;
       const int mi = lane >> 3, rr = lane & 7;
-      float sc[NT][4], sd[NT][4];  // two chains of products
+      constexpr int kChains = NT == 1 ? 2 : 1;  // two products in flight either way
+      float sc[NT][4], sd[kChains == 2 ? NT : 1][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] = sd[nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          sc[nt][e] = 0.f;
+          if constexpr (kChains == 2) sd[nt][e] = 0.f;
+        }
       {
         const int row = rbase + 8 * (mi & 1) + rr;
         uint32_t b0, b1;
@@ -612,8 +616,11 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
             for (int nt = 0; nt < NT; ++nt) {
               q_frag(0, nt, c, b0, b1);
               mma_f16_16816(sc[nt], a, b0, b1);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
               q_frag(0, nt, c + 1, b0, b1);
-              mma_f16_16816(sd[nt], b, b0, b1);
+              mma_f16_16816(kChains == 2 ? sd[kChains == 2 ? nt : 0] : sc[nt], b, b0, b1);
             }
           }
         } else {
@@ -623,12 +630,12 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
             uint32_t a0, a1, a2, a3;
             ldmatrix_x4(kbase + (d8 >> 3) * T::HALF + sw128_off(row, d8 & 7), a0, a1, a2, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              q_frag(0, nt, c, b0, b1);
-              mma_bf16_16816(sc[nt], a0, a1, a2, a3, b0, b1);
-              q_frag(NQ - 1, nt, c, b0, b1);
-              mma_bf16_16816(sd[nt], a0, a1, a2, a3, b0, b1);
-            }
+            for (int term = 0; term < NQ; ++term)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                q_frag(term, nt, c, b0, b1);
+                mma_bf16_16816(kChains == 2 && term == 1 ? sd[kChains == 2 ? nt : 0] : sc[nt], a0, a1, a2, a3, b0, b1);
+              }
           }
         }
       }
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float f = kE4M3 ? qf[nt][e & 1] * meta.y : qf[nt][e & 1];
-          const float s = (sc[nt][e] + sd[nt][e]) * f + lv;
+          const float s = (kChains == 2 ? sc[nt][e] + sd[kChains == 2 ? nt : 0][e] : sc[nt][e]) * f + lv;
           sc[nt][e] = ((e & 2) ? in1 : in0) ? s : -INFINITY;
           above |= sc[nt][e] > m[nt][e & 1] + (kLift + 8.f);
         }
