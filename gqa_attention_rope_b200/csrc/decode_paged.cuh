@@ -322,8 +322,8 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         const int ph = a.page * p.Hkv + a.g;
         r.row = ph * rpp + a.n % rpp;
         if constexpr (kE4M3) {
-          r.ks = __ldg(p.kscales + ph);
-          r.vs = __ldg(p.vscales + ph);
+          r.ks = p.kscales[ph];
+          r.vs = p.vscales[ph];
         }
       }
       return r;

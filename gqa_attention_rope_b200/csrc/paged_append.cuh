@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
 
 __device__ __forceinline__ uint4 load_row(const uint16_t* src) {
   uint4 u;  // read once: not kept in L1
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                : "l"(src));
   return u;
@@ -133,7 +133,7 @@ __device__ __forceinline__ const uint16_t* first_row(const Params& p, const Job&
 }
 // Row of a thread's i-th slot; past the end the last row again (it changes no range and is not stored).
 template <int kRowsPerPass>
-__device__ __forceinline__ int slot_row(int t0, int i, int n) {
+__device__ __forceinline__ int64_t slot_row(int t0, int i, int n) {
   return min(t0 + static_cast<int>(threadIdx.x >> 4) + i * kRowsPerPass, n - 1);
 }
 
@@ -153,7 +153,8 @@ __device__ __forceinline__ float settle_scale(const Job& j, float amax, float ol
   if (j.was > 0 && scale != old_scale) {
     const float r = old_scale / scale;
     uint4* at = reinterpret_cast<uint4*>(codes);
-    for (int i = threadIdx.x; i < j.was * 8; i += kThreads) {
+    const int64_t n = static_cast<int64_t>(j.was) * 8;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
       const uint4 c = at[i];
       at[i] = make_uint4(rescale4(c.x, r), rescale4(c.y, r), rescale4(c.z, r), rescale4(c.w, r));
     }
@@ -216,7 +217,7 @@ __device__ __forceinline__ void append_values(const Params& p, const Job& j, flo
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = t0 + row0 + i * kRowsPerPass;
-        if (r < n) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.vpages) + dst0 + r * 128) = raw[i];
+        if (r < n) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.vpages) + dst0 + static_cast<int64_t>(r) * 128) = raw[i];
       }
     }
   } else {
@@ -240,7 +241,7 @@ __device__ __forceinline__ void append_values(const Params& p, const Job& j, flo
         float x[8];
         unpack_row(raw[i], x);
         const int r = t0 + row0 + i * kRowsPerPass;
-        if (r < n) store_codes(pages + dst0 + r * 128, x, inv);
+        if (r < n) store_codes(pages + dst0 + static_cast<int64_t>(r) * 128, x, inv);
       }
     }
   }
@@ -294,8 +295,8 @@ __device__ __forceinline__ void append_keys(const Params& p, const Job& j, float
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
         const float4* c = tab + row(t0, half * kStep + i) * 32;
-        cs[i][0] = __ldg(c);
-        cs[i][1] = __ldg(c + 1);
+        cs[i][0] = c[0];
+        cs[i][1] = c[1];
       }
       if constexpr (kE4M3) {
         if (half == 0) copy_async_wait();
@@ -319,7 +320,7 @@ __device__ __forceinline__ void append_keys(const Params& p, const Job& j, float
         } else {
           const int r = t0 + row0 + s * kRowsPerPass;
           if (r < n)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kpages) + dst0 + r * 128) =
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.kpages) + dst0 + static_cast<int64_t>(r) * 128) =
                 make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                            pack_bf16x2(x[6], x[7]));
         }
@@ -354,7 +355,7 @@ __device__ __forceinline__ void append_keys(const Params& p, const Job& j, float
         const float4 u = kept(i)[0], w = kept(i)[kThreads];
         float x[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
         const int r = t0 + row0 + i * kRowsPerPass;
-        if (r < n) store_codes(pages + dst0 + r * 128, x, inv);
+        if (r < n) store_codes(pages + dst0 + static_cast<int64_t>(r) * 128, x, inv);
       }
     }
   }

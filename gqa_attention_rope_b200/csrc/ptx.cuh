@@ -130,8 +130,10 @@ __device__ __forceinline__ bool mbar_wait_backoff(uint32_t bar, uint32_t parity,
 // A kernel launched behind another with programmatic stream serialization may
 // start before that one ends. grid_dependency_wait returns once every kernel
 // it depends on has ended and its writes are visible; nothing in global memory
-// is read or written before it. grid_launch_dependents lets the next such
-// kernel start its own prologue.
+// is read or written before it, and nothing is read through the non-coherent
+// path (ld.global.nc, __ldg), whose data may not change while the kernel runs:
+// it may have begun before its inputs were written. grid_launch_dependents
+// lets the next such kernel start its own prologue.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

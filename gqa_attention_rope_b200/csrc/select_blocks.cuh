@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
       u[half][i] = make_uint4(0u, 0u, 0u, 0u);  // a block that is not there scores as zeros
       if (j0 + 4 * half + i < c1) {
         if (pg >= 0 && pg < p.n_pages)
-          u[half][i] = __ldg(reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pg) * p.Hkv + g) * 256) + lane);
+          u[half][i] = *(reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pg) * p.Hkv + g) * 256) + lane);
         else if (lane == 0)
           raise_error(LLAMA_ATTN_DEVERR_BLOCK_TABLE);
       }
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
     const int pg = table[j];
     double x = 0.0;
     if (pg >= 0 && pg < p.n_pages) {
-      const uint4 y = __ldg(reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pg) * p.Hkv + g) * 256) + lane);
+      const uint4 y = *(reinterpret_cast<const uint4*>(p.kbounds + (static_cast<int64_t>(pg) * p.Hkv + g) * 256) + lane);
       x = lane_w[0] * bf16_lo(y.x);
       x = fma(lane_w[1], bf16_hi(y.x), x);
       x = fma(lane_w[2], bf16_lo(y.y), x);

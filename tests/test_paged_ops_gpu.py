@@ -232,8 +232,7 @@ def test_append_steps_equal_one_append_but_for_subnormals(T):
 
 @pytest.mark.parametrize("page,Hkv,B,T", [(64, 8, 37, 300), (128, 4, 90, 500), (64, 1, 200, 400), (192, 3, 70, 700), (512, 2, 60, 1500)])
 def test_append_of_a_large_batch_equals_its_parts(page, Hkv, B, T):
-    """A ragged batch of many blocks at once, and sequence by sequence: the same bits. (Large and
-    small appends run on different kernels; the parts are those test_append checks.)"""
+    """A ragged batch of many blocks at once, and sequence by sequence: the same bits."""
     g = gen(T)
     lens = [int(x) for x in torch.randint(0, 3 * page, (B,), generator=g)]
     new = [int(x) for x in torch.randint(0, T + 1, (B,), generator=g)]
@@ -662,6 +661,38 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in (0, 1):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_pool_past_32_bit_offsets():
+    """A pool of more than 2^32 bytes per tensor: rows near its end, against the same rows in a small one."""
+    page, Hq, Hkv = 64, 8, 1
+    n_pages = (1 << 32) // (page * D) + 6
+    g = gen(95)
+    lens, T = [200, 77], 3
+    far = torch.tensor([[n_pages - 1, 3, n_pages - 4, n_pages - 2], [n_pages - 5, n_pages - 3, 0, 1]], dtype=torch.int32)
+    near = torch.tensor([[5, 3, 2, 4], [7, 6, 0, 1]], dtype=torch.int32)
+    small = [(torch.randn(8, Hkv, page, D, generator=g) * 64).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+             for _ in range(2)]
+    k, v = (torch.randn(2, T, Hkv, D, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(2, Hq, D, generator=g).to(torch.bfloat16).cuda()
+    rope = la.llama_attn_rope_table_build(4 * page, D, THETA)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = []
+    for table, n in ((near, 8), (far, n_pages)):
+        pools = [torch.zeros(n, Hkv, page, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.ones(n, Hkv, device="cuda") for _ in range(2)]
+        kb = torch.zeros(n, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+        for x, y in zip(pools, small):
+            x[table.flatten().long()] = y[near.flatten().long()]
+        t, after = table.cuda(), torch.empty_like(ln)
+        la.llama_attn_kv_append_paged_e4m3(k, v, *pools, *scales, t, ln, rope, kbounds=kb, out_lens=after)
+        dense = la.llama_attn_decode_paged_e4m3(q, *pools, *scales, t, after)
+        ids = la.llama_attn_select_blocks(q, kb, t, after, page, 3)
+        sparse = la.llama_attn_decode_paged_sparse_e4m3(q, *pools, *scales, t, ids, after)
+        got.append([dense, ids, sparse, kb[t.flatten().long()]] + [x[t.flatten().long()] for x in pools + scales])
+        del pools, scales, kb
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
 
 
 def test_many_sequences():
