@@ -12,14 +12,18 @@
 // range of 16 bits whatever the scales are; the denominator adds P_hn / vs_n.
 //
 // What bounds it: HBM. A row of an E4M3 cache is 256 bytes for 4 * 128 * G
-// flop. The products run on mma.sync m16n8k16 with the 16 cache rows of a warp
-// as M and the heads of the group as N (8 or 16): S^T = K Q^T, O^T = V^T P^T.
+// flop. 64 sequences of 1024 to 32768 rows, 64 heads over 8: 341 us, 6490 GB/s
+// (99% of a copy's rate); two tiles of heads (G > 8) 4600 GB/s, bound by a
+// warp's chain of conversions, products and exponentials; short caches by latency
+// (one sequence of 1000 rows, 32 heads: 8 us).
+// The products run on mma.sync m16n8k16 with the 16 cache rows of a warp as M
+// and the heads of the group as N (8 or 16): S^T = K Q^T, O^T = V^T P^T.
 // With heads as M, groups of 8 heads would leave half of each product empty.
 // E4M3 codes become f16 exactly (cvt.rn.f16x2.e4m3x2), so K and V carry no
 // rounding beyond their own; Q is rounded to f16 after its row is brought to
-// [0.5, 1) by a power of two (2^-12 relative; bf16 would be 2^-9), P to f16.
-// On bf16 pages the products are bf16: Q is the sum of two bf16 terms (2^-17
-// relative), P one bf16 (2^-9, the rounding of the output's own type).
+// [0.5, 1) by a power of two (2^-11 relative; bf16 would be 2^-8), P to f16.
+// On bf16 pages the products are bf16: Q is the sum of two bf16 terms (2^-16
+// relative), P one bf16 (2^-8, the rounding of the output's own type).
 // The 8-bit rows are loaded with the 16-bit ldmatrix: each 32-bit register
 // then holds 4 neighbouring codes of a key, or 2 codes of 2 neighbouring rows
 // of V (transposed form). The products sum over d in any order, so Q is laid
@@ -54,10 +58,12 @@ struct Tile {
   static constexpr int NT = kWide ? 2 : 1;
   static constexpr int NCW = NRW;
   static constexpr int NTHREADS = (NCW + 1) * 32;
-  // CTAs per SM. For two tiles of E4M3 (one 131072-row sequence under 128
-  // heads): 2 with the query in registers 56 us, 3 with it in shared memory
-  // (128 registers, 4 stages each) 76 us, 2 of eight compute warps with a tile
-  // each (every code converted twice) 63 us.
+  // Both tiles in one warp, 2 CTAs per SM, query in registers: one 131072-row
+  // sequence under 128 heads 58.5 us; 3 CTAs with the query in shared memory
+  // (128 registers) 76 us; a tile per warp and eight compute warps (every code
+  // converted twice) 63 us; the next stage's scores formed before this one's
+  // values (spills) 80 us. One tile for 64 heads over 8: 341 us for the 70B
+  // batch, 391 us when the empty second tile is computed along.
   static constexpr int CTAS = 2;
   static constexpr bool Q_REGS = kE4M3 || !kWide;  // query fragments in registers (two tiles of two bf16 terms: 64)
   static constexpr uint32_t HALF = ROWS * 128;                    // 64 rows x 128 bytes

@@ -22,7 +22,13 @@
 // (512 bytes read and 256 (E4M3) or 512 (bf16) written per token and head) and,
 // for E4M3 keys, issue and latency: all loads of a thread are issued before
 // the first is used, and before the page is looked up (rows past the end read
-// the last row again instead of branching).
+// the last row again instead of branching). Measured: four 8192-token prompts
+// of 8 KV heads into bf16 pages 49 us (5840 GB/s of the bytes it cannot do
+// without), a 131072-token prompt into E4M3 pages 193 us (4540 GB/s; K and V in
+// one CTA of 512 threads took 704 us). Of that prompt the keys alone take 140
+// us and the values 78: the keys' rotation, ranges, scale and coding are about
+// 12 instructions per element. A persistent form that loads the next head's
+// rows while one is coded was 4% faster on 64-row pages and slower on others.
 #pragma once
 
 #include "ptx.cuh"

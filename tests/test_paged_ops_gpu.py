@@ -15,7 +15,8 @@ bf16 2^-8, f16 2^-11, float32 2^-24, E4M3 2^-4 or 2^-10 absolute below 2^-6):
   (2^-11, and 2^-25 of 2^7 absolute: 2^-32 for each of n rows); then one bf16
   rounding of the output. With A = sum_n p_n |v_n|:
   |err| <= u |out| + A (expm1(2 delta) + 2^-10) + n 2^-32 max|v|;
-* over bf16 pages: q carries 2^-17 (two bf16 terms), a weight 2^-8.
+* over bf16 pages: q carries 2^-16 (two bf16 terms: the first leaves at most 2^-8 |x|, of
+  which the second leaves 2^-8), a weight 2^-8.
 * the log-sum-exp: delta, and float32 rounding.
 The 2^-19 (1 + |s|) covers float32 sums of 128 products (their errors are far
 below the worst case) and the exponent's and exponential's own rounding.
@@ -280,7 +281,7 @@ def test_append_leaves_refused_sequences_alone():
 # ---------------------------------------------------------------- attention
 def check_attention(kind, out, lse, ref, max_v, n_rows):
     o, ref_lse, mass, span = ref
-    u_q, u_p = (2.0 ** -11, 2.0 ** -10) if kind == "e4m3" else (2.0 ** -17, 2.0 ** -8)
+    u_q, u_p = (2.0 ** -11, 2.0 ** -10) if kind == "e4m3" else (2.0 ** -16, 2.0 ** -8)
     live = torch.isfinite(ref_lse)
     s_abs = torch.where(live, ref_lse.abs(), 0.0) + span  # |s| <= S; the exponent's reference is near the lse
     delta = u_q * span + 2.0 ** -19 * (1 + s_abs)
