@@ -540,6 +540,16 @@ def _cuda_index(name, t):
     return index
 
 
+def _empty(shape, dtype, like, stream):
+    """A new tensor on the device of ``like`` that belongs to ``stream`` (None: the current one):
+    its memory is not handed to other streams while that stream's work may use it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _call(fn, index, stream, *args):
     """Calls the library on CUDA device ``index`` (which need not be the current
     one) and that device's current stream, or on ``stream``."""
@@ -669,14 +679,13 @@ def _decode_runs(fn, q, kpages, vpages, scales, block_table, block_ids, cache_le
     _tensor("block_table", block_table, i32, (B, max_blocks), index)
     _tensor("cache_lens", cache_lens, i32, (B,), index)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(shape, torch.bfloat16, q, stream)
     _tensor("out", out, torch.bfloat16, shape, index)
     if lse is not None:
         _tensor("lse", lse, torch.float32, (B, Hq), index)
         lse = lse.data_ptr()
     if workspace is None:
-        workspace = torch.empty(max(1, llama_attn_decode_runs_workspace_size(B, Hq, Hkv, D)), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(max(1, llama_attn_decode_runs_workspace_size(B, Hq, Hkv, D)), torch.uint8, q, stream)
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace: contiguous tensor on CUDA device {index} expected")
     pools = (q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), *[t.data_ptr() for t in scales],
@@ -723,7 +732,7 @@ def llama_attn_select_blocks(q, kbounds, block_table, cache_lens, page_size: int
     _tensor("block_table", block_table, i32, (B, max_blocks), index)
     _tensor("cache_lens", cache_lens, i32, (B,), index)
     if block_ids is None:
-        block_ids = torch.empty(B, Hkv, n_sel, dtype=i32, device=q.device)
+        block_ids = _empty((B, Hkv, n_sel), i32, q, stream)
     _tensor("block_ids", block_ids, i32, (B, Hkv, n_sel), index)
     _call("llama_attn_select_blocks", index, stream, q.data_ptr(), kbounds.data_ptr(), block_table.data_ptr(),
           cache_lens.data_ptr(), block_ids.data_ptr(), B, Hq, Hkv, D, page_size, max_blocks, n_pages, n_sel, n_first,

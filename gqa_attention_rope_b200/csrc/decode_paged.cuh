@@ -49,6 +49,9 @@ namespace dpg {
 constexpr int ROWS = 64;                  // cache rows of a stage
 constexpr int NRW = 4;                    // row groups: 16 rows of a stage each
 constexpr float kLift = 7.f;              // P of the greatest row: 2^7
+// Denominators are kept in units of 2^18: with value scales down to 2^-100 a sum
+// of P / vs over 2^30 rows, P up to 2^15, stays below 2^128.
+constexpr float kSumUnit = 0x1p-18f, kSumUnitLog2 = 18.f;
 constexpr int MAX_CTAS = 512;             // runs (and twice as many partial results) the workspace holds
 
 // kWide: more than 8 query heads per KV head, two tiles of 8 (NT). Four compute
@@ -106,15 +109,17 @@ struct Params {
 };
 
 // Stages of one (sequence, KV head).
+__device__ __forceinline__ int ceil_div(int a, int b) {  // a + b may pass 2^31
+  return static_cast<int>((static_cast<unsigned>(a) + static_cast<unsigned>(b) - 1u) / static_cast<unsigned>(b));
+}
 template <bool kSparse>
 __device__ __forceinline__ int stages_of(const Params& p, int b) {
   const int len = p.lens[b];
   if (len <= 0 || len > static_cast<int64_t>(p.max_blocks) * p.page_size) return 0;
   if constexpr (kSparse) {
-    const int nb = (len + p.page_size - 1) / p.page_size;
-    return min(nb, p.n_sel) * (p.page_size / ROWS);
+    return min(ceil_div(len, p.page_size), p.n_sel) * (p.page_size / ROWS);
   }
-  return (len + ROWS - 1) / ROWS;
+  return ceil_div(len, ROWS);
 }
 
 // Position of a unit in the order (sequence, KV head, stage).
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
       Page r{a.c.g, 0, 0, 0};
       if (a.len == 0) return r;
       if constexpr (kSparse) {
-        const int spp = rpp / ROWS, e = a.c.s / spp, nb = (a.len + rpp - 1) / rpp;
+        const int spp = rpp / ROWS, e = a.c.s / spp, nb = ceil_div(a.len, rpp);
         // ascending, no id twice, -1 only behind the last one
         const bool use = a.id >= 0 && a.id < nb && (e == 0 || (a.prev >= 0 && a.prev < a.id));
         if (!use) {
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         const float vs = fminf(fmaxf(__shfl_sync(0xffffffffu, now.vs, j), 7.888609e-31f), 6.646140e35f);
         if (lane == 0 && ok) {
           *reinterpret_cast<float4*>(smem + T::OFF_META + st * 16) =
-              make_float4(__int_as_float(nvalid), ks, kE4M3 ? __log2f(vs) : 0.f, kE4M3 ? 1.f / vs : 1.f);
+              make_float4(__int_as_float(nvalid), ks, kE4M3 ? __log2f(vs) : 0.f, kE4M3 ? kSumUnit / vs : kSumUnit);
           if (nvalid > 0)
             mbar_arrive_expect_tx(full(st), T::STAGE);
           else
@@ -553,7 +558,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
           const int h = 8 * nt + 2 * t + e;
           if (h >= G) continue;
           const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
-          const float inv = L[e] == 0.f ? 0.f : 1.f / L[e];
+          const float inv = L[e] == 0.f ? 0.f : kSumUnit / L[e];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float x = o[nt][c][e], y = o[nt][c][2 + e];
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
             if (!whole)
               p.part_ml[slot * G + h] = make_float2(M[e], L[e]);
             else if (p.lse)
-              p.lse[head] = L[e] == 0.f ? -INFINITY : (M[e] + log2f(L[e])) * 0.6931471805599453f;
+              p.lse[head] = L[e] == 0.f ? -INFINITY : (M[e] + (log2f(L[e]) + kSumUnitLog2)) * 0.6931471805599453f;
           }
         }
       }
@@ -646,7 +651,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         }
       }
       const bool in0 = rbase + gq < nvalid, in1 = rbase + 8 + gq < nvalid;
-      const float lv = kE4M3 ? meta.z : 0.f, iv = kE4M3 ? meta.w : 1.f;
+      const float lv = kE4M3 ? meta.z : 0.f, iv = kE4M3 ? meta.w : kSumUnit;
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -817,10 +822,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
       float4 a;
       join_rows(p, slot, c0, c1, c0, 1, M, L, a);
       const int64_t head = static_cast<int64_t>(end.x) * p.Hq + end.y * p.G + h;
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float inv = L == 0.f ? 0.f : kSumUnit / L;
       *reinterpret_cast<uint2*>(p.out + head * 128 + 4 * lane) =
           make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-      if (p.lse && lane == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      if (p.lse && lane == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
     }
   } else {
     const int head = blockIdx.x, b = head / p.Hq, hq = head - b * p.Hq;
@@ -847,9 +852,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
     L = 0.f;
 #pragma unroll
     for (int w = 0; w < JOIN_WARPS; ++w) x += so[128 * w + threadIdx.x], L += s_l[w];
-    const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : x / L);
+    const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : x * (kSumUnit / L));
     p.out[at] = *reinterpret_cast<const uint16_t*>(&y);
-    if (p.lse && threadIdx.x == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    if (p.lse && threadIdx.x == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
   }
 }
 

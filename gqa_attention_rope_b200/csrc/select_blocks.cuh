@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
     if (g == 0 && rank == 0 && threadIdx.x == 0) raise_error(LLAMA_ATTN_DEVERR_CACHE_LEN);
     len = 0;
   }
-  const int nb = (len + p.page_size - 1) / p.page_size;
+  const int nb = static_cast<int>((static_cast<unsigned>(len) + p.page_size - 1u) / p.page_size);  // len + page_size may pass 2^31
   int32_t* ids = p.ids + bg * p.n_sel;
   if (nb <= p.n_sel) {  // every block; the whole cluster leaves here
     if (rank == 0)

@@ -367,6 +367,20 @@ def test_decode_e4m3_any_positive_scale(scale_k, scale_v):
                     448 * 1.5 * scale_v, 130)
 
 
+@pytest.mark.parametrize("scale_v", [2.0 ** -100, 2.0 ** 117])
+def test_decode_e4m3_ends_of_the_scale_range_over_many_rows(scale_v):
+    """The denominator adds weights divided by the value scale: neither end overflows or vanishes."""
+    n = 40000
+    s = attention_state("e4m3", 64, 2, 1, [n], 19, q_scale=6.0)
+    s["scales"][1] = torch.full_like(s["scales"][1], scale_v)
+    s["vv"] = R.codes(s["vp"]) * scale_v
+    d = on_gpu(s)
+    lse = torch.empty(1, 2, device="cuda")
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], lse=lse)
+    check_attention("e4m3", out, lse, R.decode(s["q"], s["kv"], s["vv"], s["table"], s["lens"], 64, THETA),
+                    448 * scale_v, n)
+
+
 @pytest.mark.parametrize("q_scale", [1e-30, 1e30, 40.0])
 def test_decode_e4m3_query_magnitudes(q_scale):
     """Queries far outside f16's range (1e30: the greatest key takes all the weight)."""
@@ -662,6 +676,31 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in (0, 1):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_memory_of_a_call_on_a_given_stream_belongs_to_that_stream():
+    """A decode without a workspace of the caller's, on a side stream that is busy: what the current
+    stream allocates and fills meanwhile is not the decode's working memory."""
+    s = attention_state("e4m3", 64, 8, 2, [3000, 900], 97)
+    d = on_gpu(s)
+    bounds = bounds_of(s).cuda()
+
+    def step(stream):
+        ids = la.llama_attn_select_blocks(d["q"], bounds, d["table"], d["lens"], 64, 9, stream=stream)
+        return la.llama_attn_decode_paged_sparse_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], ids, d["lens"],
+                                                      stream=stream)
+    want = step(None)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)  # about 25 ms
+    out = step(side)
+    sizes = [la.llama_attn_decode_runs_workspace_size(2, 8, 2), 4 * 2 * 2 * 9]
+    held = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(x.eq(0x5A).all() for x in held)
+    assert torch.equal(out, want)
 
 
 def test_pool_past_32_bit_offsets():
