@@ -517,27 +517,28 @@ def llama_attn_decode_noalloc(q, kcache, vcache, cache_lens, out, rope_theta: fl
 
 # ---- paged cache: append, E4M3 decode, block-sparse decode
 # A decode step makes several of these calls, each a few microseconds of GPU
-# work, so the checks below are written for few interpreter steps.
-def _tensor(name, t, dtype, shape, index):
-    """``t`` is a contiguous tensor of ``dtype`` and ``shape`` on CUDA device ``index``."""
-    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {index} expected, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+# work: their tensors are checked by the compiled module (csrc/binding.cpp),
+# which calls the same library. It switches to the tensors' device for the call
+# and takes that device's current stream where none is given.
+_module = None
+_entry = {}
 
 
-def _dim(name, t, n):
-    """The shape of ``t``, which has ``n`` dimensions."""
-    shape = t.shape
-    if len(shape) != n:
-        raise ValueError(f"{name}: {n} dimensions expected, got {tuple(shape)}")
-    return shape
-
-
-def _cuda_index(name, t):
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name}: CUDA tensor expected")
-    return index
+def _native():
+    global _module
+    lib_ = lib()
+    with _lock:
+        if _module is None:
+            import torch  # its libraries have to be loaded first
+            path = os.path.join(_PKG, "_binding.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"_binding.so not found at {path}; build it with "
+                                   "`python -m gqa_attention_rope_b200.build` (g++)")
+            from . import _binding
+            for name in EXPORTED:
+                _entry[name] = ctypes.cast(getattr(lib_, name), ctypes.c_void_p).value
+            _module = _binding
+    return _module
 
 
 def _empty(shape, dtype, like, stream):
@@ -550,95 +551,6 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _call(fn, index, stream, *args):
-    """Calls the library on CUDA device ``index`` (which need not be the current
-    one) and that device's current stream, or on ``stream``."""
-    import torch
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)  # torch.cuda.current_stream(index).cuda_stream
-    elif stream.device.index != index:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on device {index}")
-    else:
-        raw = stream.cuda_stream
-    f = getattr(_lib or lib(), fn)
-    if torch._C._cuda_getDevice() == index:
-        st = f(*args, raw)
-    else:
-        with torch.cuda.device(index):
-            st = f(*args, raw)
-    if st:
-        _check(fn, st)
-
-
-def _pool(kpages, vpages, scales, dtypes, D, index):
-    """Checks a page pool with its scales; (n_pages, Hkv, page_size)."""
-    import torch
-    n_pages, Hkv, page_size, _ = shape = _dim("kpages", kpages, 4)
-    dtype = kpages.dtype
-    if dtype not in dtypes or shape[3] != D:
-        raise ValueError(f"kpages: {dtypes} pages with rows of {D} expected, got {tuple(shape)} {dtype}")
-    _tensor("kpages", kpages, dtype, shape, index)
-    _tensor("vpages", vpages, dtype, shape, index)
-    if scales:
-        shape = (n_pages, Hkv)
-        _tensor("k_scales", scales[0], torch.float32, shape, index)
-        _tensor("v_scales", scales[1], torch.float32, shape, index)
-    return n_pages, Hkv, page_size
-
-
-def _kv_strides(k, v, index):
-    """(row stride, batch stride) in elements that k and v [B, T, Hkv, D] share."""
-    import torch
-    for name, t in (("k", k), ("v", v)):
-        if t.get_device() != index or t.dtype is not torch.bfloat16 or t.shape != k.shape:
-            raise ValueError(f"{name}: bfloat16 tensor of shape {tuple(k.shape)} on CUDA device {index} expected, got "
-                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    B, T, Hkv, D = k.shape
-    sb, st, sh, sd = k.stride()
-    vb, vt, vh, vd = v.stride()
-    _require((sd == vd == 1 or D == 1) and (sh == vh == D or Hkv == 1),
-             "k and v: the heads of a token must be contiguous")
-    _require((st == vt or T == 1) and (sb == vb or B == 1), "k and v must have the same strides")
-    return st if T > 1 else Hkv * D, sb if B > 1 else 0
-
-
-def _append(fn, k, v, kpages, vpages, scales, block_table, cache_lens, rope_table, new_lens, kbounds, out_lens, dtypes,
-            stream):
-    import torch
-    i32 = torch.int32
-    index = _cuda_index("k", k)
-    B, T, Hkv, D = shape = _dim("k", k, 4)
-    if k.is_contiguous() and v.is_contiguous():
-        _tensor("k", k, torch.bfloat16, shape, index)
-        _tensor("v", v, torch.bfloat16, shape, index)
-        st = Hkv * D
-        sb = T * st
-    else:
-        st, sb = _kv_strides(k, v, index)
-    n_pages, pool_heads, page_size = _pool(kpages, vpages, scales, dtypes, D, index)
-    if pool_heads != Hkv:
-        raise ValueError(f"kpages: {Hkv} KV heads expected, got {pool_heads}")
-    max_blocks = _dim("block_table", block_table, 2)[1]
-    _tensor("block_table", block_table, i32, (B, max_blocks), index)
-    _tensor("cache_lens", cache_lens, i32, (B,), index)
-    rows = _dim("rope_table", rope_table, 3)[0]
-    _tensor("rope_table", rope_table, torch.float32, (rows, D // 2, 2), index)
-    new = out = bounds = None
-    if new_lens is not None:
-        _tensor("new_lens", new_lens, i32, (B,), index)
-        new = new_lens.data_ptr()
-    if out_lens is not None:
-        _tensor("out_lens", out_lens, i32, (B,), index)
-        out = out_lens.data_ptr()
-    if kbounds is not None:
-        _tensor("kbounds", kbounds, torch.bfloat16, (n_pages, Hkv, 2, D), index)
-        bounds = kbounds.data_ptr()
-    _call(fn, index, stream, k.data_ptr(), v.data_ptr(), st, sb, kpages.data_ptr(), vpages.data_ptr(),
-          *[t.data_ptr() for t in scales], bounds, block_table.data_ptr(), cache_lens.data_ptr(), new, out, B, T, Hkv,
-          D, page_size, max_blocks, n_pages, rope_table.data_ptr(), rows)
-    return out_lens
-
-
 def llama_attn_kv_append_paged(k, v, kpages, vpages, block_table, cache_lens, rope_table, new_lens=None, kbounds=None,
                                out_lens=None, stream=None):
     """Appends k and v [B,T,Hkv,128] (bf16, un-rotated; slices of a fused
@@ -648,18 +560,24 @@ def llama_attn_kv_append_paged(k, v, kpages, vpages, block_table, cache_lens, ro
     rows). new_lens int32 [B]: rows per sequence where they are fewer than T.
     kbounds bf16 [n_pages,Hkv,2,128]: per block least and greatest key, kept for
     llama_attn_select_blocks. out_lens int32 [B] gets the new lengths. Returns out_lens."""
-    import torch
-    return _append("llama_attn_kv_append_paged", k, v, kpages, vpages, (), block_table, cache_lens, rope_table,
-                   new_lens, kbounds, out_lens, (torch.bfloat16,), stream)
+    module = _module or _native()
+    st = module.append(_entry["llama_attn_kv_append_paged"], 0, k, v, kpages, vpages, block_table, cache_lens,
+                       rope_table, new_lens, kbounds, out_lens, stream)
+    if st:
+        _check("llama_attn_kv_append_paged", st)
+    return out_lens
 
 
 def llama_attn_kv_append_paged_e4m3(k, v, kpages, vpages, k_scales, v_scales, block_table, cache_lens, rope_table,
                                     new_lens=None, kbounds=None, out_lens=None, stream=None):
     """llama_attn_kv_append_paged into E4M3 pages (uint8 or float8_e4m3fn) with
     one float32 scale per page and KV head, k_scales and v_scales [n_pages,Hkv]."""
-    import torch
-    return _append("llama_attn_kv_append_paged_e4m3", k, v, kpages, vpages, (k_scales, v_scales), block_table,
-                   cache_lens, rope_table, new_lens, kbounds, out_lens, (torch.uint8, torch.float8_e4m3fn), stream)
+    module = _module or _native()
+    st = module.append(_entry["llama_attn_kv_append_paged_e4m3"], 1, k, v, kpages, vpages, k_scales, v_scales,
+                       block_table, cache_lens, rope_table, new_lens, kbounds, out_lens, stream)
+    if st:
+        _check("llama_attn_kv_append_paged_e4m3", st)
+    return out_lens
 
 
 def llama_attn_decode_runs_workspace_size(B: int, Hq: int, Hkv: int, D: int = 128) -> int:
@@ -667,37 +585,21 @@ def llama_attn_decode_runs_workspace_size(B: int, Hq: int, Hkv: int, D: int = 12
     return int(lib().llama_attn_decode_runs_workspace_size(int(B), int(Hq), int(Hkv), int(D)))
 
 
-def _decode_runs(fn, q, kpages, vpages, scales, block_table, block_ids, cache_lens, out, lse, workspace, q_pos_offset,
-                 rope_theta, dtypes, stream):
-    import torch
-    i32 = torch.int32
-    index = _cuda_index("q", q)
-    B, Hq, D = shape = _dim("q", q, 3)
-    _tensor("q", q, torch.bfloat16, shape, index)
-    n_pages, Hkv, page_size = _pool(kpages, vpages, scales, dtypes, D, index)
-    max_blocks = _dim("block_table", block_table, 2)[1]
-    _tensor("block_table", block_table, i32, (B, max_blocks), index)
-    _tensor("cache_lens", cache_lens, i32, (B,), index)
-    if out is None:
-        out = _empty(shape, torch.bfloat16, q, stream)
-    _tensor("out", out, torch.bfloat16, shape, index)
-    if lse is not None:
-        _tensor("lse", lse, torch.float32, (B, Hq), index)
-        lse = lse.data_ptr()
-    if workspace is None:
-        workspace = _empty(max(1, llama_attn_decode_runs_workspace_size(B, Hq, Hkv, D)), torch.uint8, q, stream)
-    if workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace: contiguous tensor on CUDA device {index} expected")
-    pools = (q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), *[t.data_ptr() for t in scales],
-             block_table.data_ptr())
-    sizes = (out.data_ptr(), lse, B, Hq, Hkv, D, page_size, max_blocks, n_pages)
-    tail = (q_pos_offset, rope_theta, workspace.data_ptr(), workspace.nbytes)
-    if block_ids is None:
-        _call(fn, index, stream, *pools, cache_lens.data_ptr(), *sizes, *tail)
-    else:
-        n_sel = _dim("block_ids", block_ids, 3)[2]
-        _tensor("block_ids", block_ids, i32, (B, Hkv, n_sel), index)
-        _call(fn, index, stream, *pools, block_ids.data_ptr(), cache_lens.data_ptr(), *sizes, n_sel, *tail)
+def _decode_runs(fn, q, pool, block_table, block_ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream):
+    module = _module or _native()
+    if out is None or workspace is None:
+        import torch
+        if q.dim() != 3 or pool[0].dim() != 4 or not q.is_cuda:
+            raise ValueError("CUDA tensors q [B, Hq, 128] and pages [n_pages, Hkv, page_size, 128] expected")
+        if out is None:
+            out = _empty(q.shape, torch.bfloat16, q, stream)
+        if workspace is None:
+            need = llama_attn_decode_runs_workspace_size(q.shape[0], q.shape[1], pool[0].shape[1], q.shape[2])
+            workspace = _empty(max(1, need), torch.uint8, q, stream)
+    st = module.decode(_entry[fn], len(pool) == 4, q, *pool, block_table, block_ids, cache_lens, out, lse, workspace,
+                       q_pos_offset, rope_theta, stream)
+    if st:
+        _check(fn, st)
     return out
 
 
@@ -708,10 +610,8 @@ def llama_attn_decode_paged_e4m3(q, kpages, vpages, k_scales, v_scales, block_ta
     rotated at cache_lens[b] + q_pos_offset: 0 as in llama_attn_decode, -1 where
     its own key has been appended. lse float32 [B,Hq] (optional) gets the
     log-sum-exp. Returns out [B,Hq,128]."""
-    import torch
-    return _decode_runs("llama_attn_decode_paged_e4m3", q, kpages, vpages, (k_scales, v_scales), block_table, None,
-                        cache_lens, out, lse, workspace, q_pos_offset, rope_theta,
-                        (torch.uint8, torch.float8_e4m3fn), stream)
+    return _decode_runs("llama_attn_decode_paged_e4m3", q, (kpages, vpages, k_scales, v_scales), block_table, None,
+                        cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream)
 
 
 def llama_attn_select_blocks(q, kbounds, block_table, cache_lens, page_size: int, n_sel: int, n_first: int = 1,
@@ -721,22 +621,16 @@ def llama_attn_select_blocks(q, kbounds, block_table, cache_lens, page_size: int
     the first n_first, the last n_last, and those with the greatest bound of
     the group's products with a key of the block (kbounds, as the append keeps
     them). Returns block_ids int32 [B,Hkv,n_sel], ascending, -1 behind the last."""
-    import torch
-    i32 = torch.int32
-    index = _cuda_index("q", q)
-    B, Hq, D = shape = _dim("q", q, 3)
-    _tensor("q", q, torch.bfloat16, shape, index)
-    n_pages, Hkv, _, _ = _dim("kbounds", kbounds, 4)
-    _tensor("kbounds", kbounds, torch.bfloat16, (n_pages, Hkv, 2, D), index)
-    max_blocks = _dim("block_table", block_table, 2)[1]
-    _tensor("block_table", block_table, i32, (B, max_blocks), index)
-    _tensor("cache_lens", cache_lens, i32, (B,), index)
+    module = _module or _native()
     if block_ids is None:
-        block_ids = _empty((B, Hkv, n_sel), i32, q, stream)
-    _tensor("block_ids", block_ids, i32, (B, Hkv, n_sel), index)
-    _call("llama_attn_select_blocks", index, stream, q.data_ptr(), kbounds.data_ptr(), block_table.data_ptr(),
-          cache_lens.data_ptr(), block_ids.data_ptr(), B, Hq, Hkv, D, page_size, max_blocks, n_pages, n_sel, n_first,
-          n_last, q_pos_offset, rope_theta)
+        import torch
+        if q.dim() != 3 or kbounds.dim() != 4 or not q.is_cuda:
+            raise ValueError("CUDA tensors q [B, Hq, 128] and kbounds [n_pages, Hkv, 2, 128] expected")
+        block_ids = _empty((q.shape[0], kbounds.shape[1], max(0, n_sel)), torch.int32, q, stream)
+    st = module.select(_entry["llama_attn_select_blocks"], q, kbounds, block_table, cache_lens, block_ids, page_size,
+                       n_sel, n_first, n_last, q_pos_offset, rope_theta, stream)
+    if st:
+        _check("llama_attn_select_blocks", st)
     return block_ids
 
 
@@ -746,19 +640,16 @@ def llama_attn_decode_paged_sparse(q, kpages, vpages, block_table, block_ids, ca
     bf16 page pool (ascending, each once, -1 behind the last; as
     llama_attn_select_blocks gives them). Other arguments as for
     llama_attn_decode_paged_e4m3. Returns out [B,Hq,128]."""
-    import torch
-    return _decode_runs("llama_attn_decode_paged_sparse", q, kpages, vpages, (), block_table, block_ids, cache_lens,
-                        out, lse, workspace, q_pos_offset, rope_theta, (torch.bfloat16,), stream)
+    return _decode_runs("llama_attn_decode_paged_sparse", q, (kpages, vpages), block_table, block_ids, cache_lens, out,
+                        lse, workspace, q_pos_offset, rope_theta, stream)
 
 
 def llama_attn_decode_paged_sparse_e4m3(q, kpages, vpages, k_scales, v_scales, block_table, block_ids, cache_lens,
                                         out=None, lse=None, workspace=None, q_pos_offset: int = 0,
                                         rope_theta: float = 500000.0, stream=None):
     """llama_attn_decode_paged_sparse over an E4M3 page pool with its scales."""
-    import torch
-    return _decode_runs("llama_attn_decode_paged_sparse_e4m3", q, kpages, vpages, (k_scales, v_scales), block_table,
-                        block_ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta,
-                        (torch.uint8, torch.float8_e4m3fn), stream)
+    return _decode_runs("llama_attn_decode_paged_sparse_e4m3", q, (kpages, vpages, k_scales, v_scales), block_table,
+                        block_ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream)
 
 
 def shard_units(n_units: int, world_size: int, rank: int):

@@ -1,4 +1,5 @@
-"""Builds the CUDA library libllama_attn.so in-tree for sm_100a (nvcc)."""
+"""Builds the CUDA library libllama_attn.so for sm_100a (nvcc) and the Python
+module _binding.so that calls its paged-cache entry points (g++), in-tree."""
 from __future__ import annotations
 
 import os
@@ -10,6 +11,8 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "llama_attn.cu")
 LIB = os.path.join(PKG, "libllama_attn.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 
 def sources():
@@ -23,10 +26,29 @@ def nvcc_command(out: str = LIB, extra=()):
             "-shared", "-Xcompiler", "-fPIC", "-I" + INCLUDE, *extra, "-o", out, SRC]
 
 
+def binding_command(out: str = BINDING):
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+            "-I" + os.path.join(base, "include"), "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), BINDING_SRC, "-o", out,
+            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
+def _stale(target: str, files) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in files)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    stale = force or not os.path.exists(LIB) or any(
-        os.path.getmtime(f) > os.path.getmtime(LIB) for f in sources())
-    if stale:
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "llama_attn.h")]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        subprocess.check_call(binding_command(tmp))
+        os.replace(tmp, BINDING)
+    if force or _stale(LIB, sources()):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = nvcc_command(tmp, ["-Xptxas", "-v"] if verbose else [])
         subprocess.check_call(cmd)

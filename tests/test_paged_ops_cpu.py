@@ -123,27 +123,31 @@ def test_runs_workspace_size(lib):
     assert f(1, 16, 1, 128) < 10 << 20  # whatever the lengths
 
 
-def test_binding_refuses_before_the_library():
+def test_binding_refuses_before_the_library(lib):
     x = torch.zeros(1, 1, 1, 128, dtype=torch.bfloat16)
     lens = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA tensor"):
         la.llama_attn_kv_append_paged(x, x, x, x, lens[None], lens, x)
     with pytest.raises(ValueError, match="CUDA tensor"):
+        la.llama_attn_kv_append_paged_e4m3(x, x, x, x, x, x, lens[None], lens, x)
+    with pytest.raises(ValueError, match="CUDA tensor"):
         la.llama_attn_decode_paged_sparse(x[0], x, x, lens[None], lens[None, None], lens)
     with pytest.raises(ValueError, match="CUDA tensor"):
+        la.llama_attn_decode_paged_e4m3(x[0], x, x, x, x, lens[None], lens, out=x[0], workspace=x)
+    with pytest.raises(ValueError, match="CUDA tensor"):
         la.llama_attn_select_blocks(x[0], x, lens[None], lens, 64, 4)
+    with pytest.raises(ValueError, match="k: tensor expected"):
+        la.llama_attn_kv_append_paged(None, x, x, x, lens[None], lens, x)
+    with pytest.raises(ValueError, match="too few arguments"):
+        la._native().append(la._entry["llama_attn_kv_append_paged"], 0, x)
 
 
-def test_binding_checks_each_tensor():
-    t = torch.zeros(2, 3, dtype=torch.int32)
-    la._tensor("t", t, torch.int32, (2, 3), -1)  # device index -1: CPU
-    for bad in (t.float(), t[0], t[:, :2], t.T.contiguous().T, torch.zeros(3, 3, dtype=torch.int32)):
-        with pytest.raises(ValueError, match="t: "):
-            la._tensor("t", bad, torch.int32, (2, 3), -1)
-    with pytest.raises(ValueError, match="on CUDA device 0 expected"):
-        la._tensor("t", t, torch.int32, (2, 3), 0)
-    with pytest.raises(ValueError, match="3 dimensions expected"):
-        la._dim("t", t, 3)
+def test_binding_fails_loudly_when_it_is_not_built(lib, monkeypatch, tmp_path):
+    la.lib()
+    monkeypatch.setattr(la, "_module", None)
+    monkeypatch.setattr(la, "_PKG", str(tmp_path))
+    with pytest.raises(RuntimeError, match="_binding.so not found"):
+        la._native()
 
 
 # ---- the statements the GPU tests rely on

@@ -735,6 +735,63 @@ def test_pool_past_32_bit_offsets():
         assert torch.equal(x, y)
 
 
+def test_binding_checks_every_tensor():
+    """One wrong thing at a time: each is refused by name before the library is called."""
+    page, Hq, Hkv, B, T, n_pages = 64, 4, 2, 2, 3, 5
+
+    def z(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    good = dict(k=z(B, T, Hkv, D), v=z(B, T, Hkv, D), kpages=z(n_pages, Hkv, page, D, dtype=u8),
+                vpages=z(n_pages, Hkv, page, D, dtype=u8), k_scales=z(n_pages, Hkv, dtype=f32),
+                v_scales=z(n_pages, Hkv, dtype=f32), block_table=z(B, 2, dtype=i32), cache_lens=z(B, dtype=i32),
+                rope_table=z(2 * page, D // 2, 2, dtype=f32), new_lens=z(B, dtype=i32),
+                kbounds=z(n_pages, Hkv, 2, D), out_lens=z(B, dtype=i32))
+    good["block_table"][1] = 2
+    la.llama_attn_kv_append_paged_e4m3(**good)
+    read = dict(q=z(B, Hq, D), **{n: good[n] for n in ("kpages", "vpages", "k_scales", "v_scales", "block_table",
+                                                       "cache_lens")},
+                block_ids=z(B, Hkv, 3, dtype=i32), out=z(B, Hq, D), lse=z(B, Hq, dtype=f32))
+    la.llama_attn_decode_paged_sparse_e4m3(**read)
+    choose = dict(q=read["q"], kbounds=good["kbounds"], block_table=good["block_table"],
+                  cache_lens=good["cache_lens"], block_ids=read["block_ids"])
+    la.llama_attn_select_blocks(**choose, page_size=page, n_sel=3)
+
+    def spoiled(t):
+        other = torch.float16 if t.dtype == torch.bfloat16 else torch.int64 if t.dtype == i32 else torch.float64
+        yield t.to(other)
+        yield t.cpu()
+        yield torch.cat([t, t])
+        yield t[..., None]
+        if t.dim() > 1:
+            yield t.transpose(0, 1).contiguous().transpose(0, 1)
+    for call, args, more in ((la.llama_attn_kv_append_paged_e4m3, good, {}),
+                             (la.llama_attn_decode_paged_sparse_e4m3, read, {}),
+                             (la.llama_attn_select_blocks, choose, dict(page_size=page, n_sel=3))):
+        for name in args:
+            for bad in spoiled(args[name]):
+                if name in ("k", "v") and bad.dim() == 4 and bad.shape == args[name].shape and bad.is_cuda \
+                        and bad.dtype == args[name].dtype:
+                    continue  # strides of k and v are free as long as they agree
+                if name == "rope_table" and bad.shape[0] > args[name].shape[0]:
+                    continue  # a table may have more rows than the cache
+                if call is la.llama_attn_select_blocks and name == "kbounds" and bad.shape[0] > n_pages:
+                    continue  # the selection knows the pool by its bounds only
+                with pytest.raises(ValueError):
+                    call(**{**args, name: bad}, **more)
+    with pytest.raises(ValueError, match="same strides"):
+        la.llama_attn_kv_append_paged_e4m3(**{**good, "v": z(T, B, Hkv, D).transpose(0, 1)})
+    with pytest.raises(ValueError, match="heads of a token"):
+        la.llama_attn_kv_append_paged_e4m3(**{**good, "v": z(B, T, D, Hkv).transpose(2, 3)})
+    with pytest.raises(ValueError, match="bfloat16 pages"):
+        la.llama_attn_decode_paged_sparse(**{n: x for n, x in read.items() if n not in ("k_scales", "v_scales")})
+    with pytest.raises(la.LlamaAttnError):
+        la.llama_attn_select_blocks(**choose, page_size=page, n_sel=3, n_first=4)
+    with pytest.raises(la.LlamaAttnError):
+        la.llama_attn_decode_paged_sparse_e4m3(**{**read, "out": read["q"]})
+    assert la.llama_attn_get_device_error() == 0
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, most of them empty or short."""
     g = gen(91)
