@@ -425,11 +425,6 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
   // The rotated query rows of (b, g) as B fragments of the score product.
   auto load_query = [&]() {
     float2* cs_row = reinterpret_cast<float2*>(smem + T::OFF_CS);
-    if (threadIdx.x < 64) {
-      double sn, cs;
-      sincos(static_cast<double>(p.lens[cur.b] + p.q_pos_offset) * p.freqs.theta[threadIdx.x], &sn, &cs);
-      cs_row[threadIdx.x] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
-    }
     uint2 u[2 * NT];  // a warp stages two heads of each tile
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
@@ -437,6 +432,11 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
       u[i] = make_uint2(0u, 0u);
       if (h < G)
         u[i] = *reinterpret_cast<const uint2*>(p.q + (static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h) * 128 + 4 * lane);
+    }
+    if (threadIdx.x < 64) {
+      double sn, cs;
+      sincos(static_cast<double>(p.lens[cur.b] + p.q_pos_offset) * p.freqs.theta[threadIdx.x], &sn, &cs);
+      cs_row[threadIdx.x] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
     }
     bar();
     const float4 cs = reinterpret_cast<const float4*>(cs_row)[lane];
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
   };
 
   // Joins the four warps' results of the segment that ends here, and writes it.
-  auto finish = [&](int first_unit, int last_unit) {
+  auto finish = [&](int first_unit, int last_unit, bool last) {  // last: of this run
     float2* ml = reinterpret_cast<float2*>(smem + T::OFF_ML);  // [warp][head]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -504,30 +504,86 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         if (gq == 0) ml[warp * 16 + 8 * nt + 2 * t + e] = make_float2(m[nt][e], s);
       }
     bar();
-    float4* scr = reinterpret_cast<float4*>(smem + T::OFF_SCR);
     const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
     if (first_unit < u0 && last_unit <= u1 && threadIdx.x == 0)
       p.ends[blockIdx.x] = make_int4(cur.b, cur.g, cut.run_of(first_unit), 0);
+    // A head's denominator and reference over the four warps, and this warp's factor.
+    auto head_of = [&](int h, float& M, float& L) {
+      float2 v[NCW];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float M[2], L[2];
+      for (int w = 0; w < NCW; ++w) v[w] = ml[w * 16 + h];
+      M = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+      L = 0.f;
+#pragma unroll
+      for (int w = 0; w < NCW; ++w) L += v[w].x == -INFINITY ? v[w].y : v[w].y * ex2_approx(v[w].x - M);  // no row: 0 (or a NaN)
+    };
+    auto store_stats = [&](int h, float M, float L) {
+      if (!whole)
+        p.part_ml[slot * G + h] = make_float2(M, L);
+      else if (p.lse)
+        p.lse[static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h] =
+            L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float2 v[NCW];
-#pragma unroll
-        for (int w = 0; w < NCW; ++w) v[w] = ml[w * 16 + 8 * nt + 2 * t + e];
-        M[e] = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-        L[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < NCW; ++w) L[e] += v[w].x == -INFINITY ? v[w].y : v[w].y * ex2_approx(v[w].x - M[e]);  // no row: 0 (or a NaN)
-        const float f = m[nt][e] == -INFINITY ? 1.f : ex2_approx(m[nt][e] - M[e]);
+        float M, L;
+        head_of(8 * nt + 2 * t + e, M, L);
+        const float f = m[nt][e] == -INFINITY ? 1.f : ex2_approx(m[nt][e] - M);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           o[nt][c][e] *= f;
           o[nt][c][2 + e] *= f;
         }
       }
+    if (last) {
+      // No copy will fill the ring again: all warps put their rows there
+      // ([warp][head][channel], rows of 132 floats) and every thread sums a part.
+      constexpr int kRow = 132;
+      float* ring = reinterpret_cast<float*>(smem);
+      static_assert(NCW * 8 * NT * kRow * 4 <= static_cast<int>(T::OFF_Q), "the partial rows fit into the ring");
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* row = ring + (warp * 8 * NT + 8 * nt + 2 * t + e) * kRow;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if constexpr (kE4M3) {  // channels 16c + 2gq, + 1
+              *reinterpret_cast<float2*>(row + 16 * c + 2 * gq) = make_float2(o[nt][c][e], o[nt][c][2 + e]);
+            } else {  // channels 16c + gq and 16c + 8 + gq
+              row[16 * c + gq] = o[nt][c][e];
+              row[16 * c + 8 + gq] = o[nt][c][2 + e];
+            }
+          }
+        }
+      bar();
+      for (int h = warp; h < G; h += NCW) {  // a warp a head, a lane 4 channels
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NCW; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(ring + (w * 8 * NT + h) * kRow + 4 * lane);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        float M, L;
+        head_of(h, M, L);
+        if (whole) {
+          const float inv = L == 0.f ? 0.f : kSumUnit / L;
+          const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
+          *reinterpret_cast<uint2*>(p.out + head * 128 + 4 * lane) =
+              make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + (slot * G + h) * 128 + 4 * lane) = x;
+        }
+        if (lane == 0) store_stats(h, M, L);
+      }
+      return;
+    }
+    float4* scr = reinterpret_cast<float4*>(smem + T::OFF_SCR);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       // the scratch holds two warps' channels of half the chunks
 #pragma unroll
       for (int c0 = 0; c0 < 8; c0 += 4) {
@@ -557,17 +613,19 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         for (int e = 0; e < 2; ++e) {
           const int h = 8 * nt + 2 * t + e;
           if (h >= G) continue;
+          float M, L;
+          head_of(h, M, L);
           const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
-          const float inv = L[e] == 0.f ? 0.f : kSumUnit / L[e];
+          const float inv = L == 0.f ? 0.f : kSumUnit / L;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float x = o[nt][c][e], y = o[nt][c][2 + e];
-            if constexpr (kE4M3) {  // channels 16c + 2gq, + 1
+            if constexpr (kE4M3) {
               if (whole)
                 *reinterpret_cast<uint32_t*>(p.out + head * 128 + 16 * c + 2 * gq) = pack_bf16x2(x * inv, y * inv);
               else
                 *reinterpret_cast<float2*>(p.part_o + (slot * G + h) * 128 + 16 * c + 2 * gq) = make_float2(x, y);
-            } else {  // channels 16c + gq and 16c + 8 + gq
+            } else {
               if (whole) {
                 const uint32_t w = pack_bf16x2(x * inv, y * inv);
                 p.out[head * 128 + 16 * c + gq] = static_cast<uint16_t>(w & 0xFFFFu);
@@ -578,12 +636,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
               }
             }
           }
-          if (gq == 0) {
-            if (!whole)
-              p.part_ml[slot * G + h] = make_float2(M[e], L[e]);
-            else if (p.lse)
-              p.lse[head] = L[e] == 0.f ? -INFINITY : (M[e] + (log2f(L[e]) + kSumUnitLog2)) * 0.6931471805599453f;
-          }
+          if (gq == 0) store_stats(h, M, L);
         }
       }
     }
@@ -742,7 +795,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     __syncwarp();
     if (alive && lane == 0) mbar_arrive(empty(st));
     if (cur.s + 1 == cur.nst || i + 1 == n_units) {
-      finish(seg_first, seg_first + cur.nst);
+      finish(seg_first, seg_first + cur.nst, i + 1 == n_units);
       if (i + 1 < n_units) {
         advance<kSparse>(p, cur, 1);
         seg_first = u0 + i + 1;

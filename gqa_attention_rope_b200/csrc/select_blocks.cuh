@@ -357,14 +357,13 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
     return x > hi ? 2 : x < lo ? 0 : 1;
   };
   const int nb32 = (nb + 31) & ~31;
+  int mine_in = 0;
+#pragma unroll 4
   for (int j0 = warp * 32; j0 < nb32; j0 += NTHREADS) {
     const int j = j0 + lane, d = j < nb ? decide(j) : 0;
     const unsigned in = __ballot_sync(0xffffffffu, d == 2), near = __ballot_sync(0xffffffffu, d == 1);
-    if (lane == 0) {
-      s_in[j0 >> 5] = in;
-      s_eq[j0 >> 5] = 0u;
-      if (in) atomicAdd(&s_n_in, __popc(in));
-    }
+    mine_in += __popc(in);
+    if (lane == 0) s_in[j0 >> 5] = in, s_eq[j0 >> 5] = 0u;
     if (near) {
       int at = 0;
       if (lane == 0) at = atomicAdd(&s_n_near, __popc(near));
@@ -372,6 +371,7 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
       if (d == 1 && at < kNearCap) s_near[at] = j;
     }
   }
+  if (lane == 0 && mine_in) atomicAdd(&s_n_in, mine_in);
   __syncthreads();
   const int n_near = s_n_near;
   int take = p.n_sel - s_n_in;  // of the near ones
