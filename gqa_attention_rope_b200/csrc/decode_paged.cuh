@@ -194,7 +194,10 @@ __device__ __forceinline__ void clear_empty(const Params& p, int n) {
 }
 
 // kWide: more than 8 query heads per KV head (two tiles of 8).
-template <bool kE4M3, bool kSparse, bool kWide>
+// kCluster: a cluster of CTAs per (sequence, KV head) instead of runs over the
+// batch; they cut the pair's stages among themselves and join their results
+// through one another's shared memory, so nothing is left for a second kernel.
+template <bool kE4M3, bool kSparse, bool kWide, bool kCluster>
 __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, kWide>::CTAS))
     decode_runs_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const Params p) {
@@ -209,9 +212,6 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wc{p.epoch};
 
-  __shared__ int4 s_start;
-  __shared__ int s_part[NTHREADS];
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::NSTAGE; ++s) {
       mbar_init(full(s), 1);
@@ -223,51 +223,81 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  // Units before this thread's share of the sequences, and in all: thread i
-  // takes sequences [i * per, (i + 1) * per).
-  const int per = (p.B + NTHREADS - 1) / NTHREADS;
-  const int my0 = min(p.B, static_cast<int>(threadIdx.x) * per), my1 = min(p.B, my0 + per);
-  {
-    int sum = 0;
-    for (int b = my0; b < my1; ++b) sum += stages_of<kSparse>(p, b) * p.Hkv;
-    s_part[threadIdx.x] = sum;
-  }
-  __syncthreads();
-  int before = 0, total = 0;
-  for (int i = 0; i < NTHREADS && i * per < p.B; ++i) {
-    if (i == static_cast<int>(threadIdx.x)) before = total;
-    total += s_part[i];
-  }
-  if (my0 < p.B && blockIdx.x == 0) {  // the joining kernel reads these
-    int at = before;
-    for (int b = my0; b < my1; ++b) {
-      p.prefix[b] = at;
-      at += stages_of<kSparse>(p, b) * p.Hkv;
-    }
-    if (my1 == p.B) p.prefix[p.B] = at;
-  }
-  if (threadIdx.x == 0) p.ends[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  const int n_runs = min(static_cast<int>(gridDim.x), total);
-  if (static_cast<int>(blockIdx.x) >= n_runs) {
-    clear_empty<kSparse>(p, NTHREADS);
-    return;
-  }
-  const Cut cut(total, n_runs);
-  const int u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
-  if (my0 < my1 && before <= u0 && u0 < before + s_part[threadIdx.x]) {  // one thread finds the start
-    int at = before;
-    for (int b = my0; b < my1; ++b) {
-      const int nst = stages_of<kSparse>(p, b), n = nst * p.Hkv;
-      if (u0 < at + n) {
-        const int g = (u0 - at) / nst;
-        s_start = make_int4(b, g, u0 - at - g * nst, nst);
-        break;
+  Cut cut(1, 1);
+  int u0 = 0, u1 = 0;  // this CTA's units
+  Cursor cur;
+  const uint32_t rank = kCluster ? cluster_rank() : 0u, csize = kCluster ? cluster_size() : 1u;
+  if constexpr (kCluster) {
+    const int pair = blockIdx.x / csize;
+    cur = Cursor{pair / p.Hkv, pair % p.Hkv, 0, 0};
+    cur.nst = stages_of<kSparse>(p, cur.b);
+    if (cur.nst == 0) {  // no rows: zeros, and the whole cluster leaves
+      if (rank == 0) {
+        const int len = p.lens[cur.b];
+        if (threadIdx.x == 0 && cur.g == 0 && (len < 0 || len > static_cast<int64_t>(p.max_blocks) * p.page_size))
+          raise_error(LLAMA_ATTN_DEVERR_CACHE_LEN);
+        const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * p.G;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + head * 128);
+        for (int i = threadIdx.x; i < p.G * 64; i += NTHREADS) dst[i] = 0u;
+        if (p.lse && static_cast<int>(threadIdx.x) < p.G) p.lse[head + threadIdx.x] = -INFINITY;
       }
-      at += n;
+      return;
     }
+    __syncthreads();  // the barriers are there
+    const int n_runs = min(static_cast<int>(csize), cur.nst);
+    cut = Cut(cur.nst, n_runs);
+    if (static_cast<int>(rank) < n_runs) u0 = cut.start(rank), u1 = cut.start(rank + 1);
+    cur.s = u0;
+  } else {
+    __shared__ int4 s_start;
+    __shared__ int s_part[NTHREADS];
+    // Units before this thread's share of the sequences, and in all: thread i
+    // takes sequences [i * per, (i + 1) * per).
+    const int per = (p.B + NTHREADS - 1) / NTHREADS;
+    const int my0 = min(p.B, static_cast<int>(threadIdx.x) * per), my1 = min(p.B, my0 + per);
+    {
+      int sum = 0;
+      for (int b = my0; b < my1; ++b) sum += stages_of<kSparse>(p, b) * p.Hkv;
+      s_part[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int i = 0; i < NTHREADS && i * per < p.B; ++i) {
+      if (i == static_cast<int>(threadIdx.x)) before = total;
+      total += s_part[i];
+    }
+    if (my0 < p.B && blockIdx.x == 0) {  // the joining kernel reads these
+      int at = before;
+      for (int b = my0; b < my1; ++b) {
+        p.prefix[b] = at;
+        at += stages_of<kSparse>(p, b) * p.Hkv;
+      }
+      if (my1 == p.B) p.prefix[p.B] = at;
+    }
+    if (threadIdx.x == 0) p.ends[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    const int n_runs = min(static_cast<int>(gridDim.x), total);
+    if (static_cast<int>(blockIdx.x) >= n_runs) {
+      clear_empty<kSparse>(p, NTHREADS);
+      return;
+    }
+    cut = Cut(total, n_runs);
+    u0 = cut.start(blockIdx.x);
+    u1 = cut.start(blockIdx.x + 1);
+    if (my0 < my1 && before <= u0 && u0 < before + s_part[threadIdx.x]) {  // one thread finds the start
+      int at = before;
+      for (int b = my0; b < my1; ++b) {
+        const int nst = stages_of<kSparse>(p, b), n = nst * p.Hkv;
+        if (u0 < at + n) {
+          const int g = (u0 - at) / nst;
+          s_start = make_int4(b, g, u0 - at - g * nst, nst);
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    cur = Cursor{s_start.x, s_start.y, s_start.z, s_start.w};
   }
-  __syncthreads();
-  Cursor cur{s_start.x, s_start.y, s_start.z, s_start.w};
 
   if (warp == NCW) {
     // ------------------------------------------------------------ producer
@@ -394,6 +424,11 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     if (lane == 0)  // copies in flight land before the CTA's shared memory goes
       for (int st = 0; st < T::NSTAGE; ++st)
         if (done > st) mbar_wait(full(st), ((done - 1 - st) / T::NSTAGE) & 1, wc);
+    if constexpr (kCluster) {  // with the compute warps: results written, results read
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
@@ -506,7 +541,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     bar();
     const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
-    if (first_unit < u0 && last_unit <= u1 && threadIdx.x == 0)
+    if (!kCluster && first_unit < u0 && last_unit <= u1 && threadIdx.x == 0)
       p.ends[blockIdx.x] = make_int4(cur.b, cur.g, cut.run_of(first_unit), 0);
     // A head's denominator and reference over the four warps, and this warp's factor.
     auto head_of = [&](int h, float& M, float& L) {
@@ -543,7 +578,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
       // ([warp][head][channel], rows of 132 floats) and every thread sums a part.
       constexpr int kRow = 132;
       float* ring = reinterpret_cast<float*>(smem);
-      static_assert(NCW * 8 * NT * kRow * 4 <= static_cast<int>(T::OFF_Q), "the partial rows fit into the ring");
+      static_assert((NCW + 1) * 8 * NT * kRow * 4 <= static_cast<int>(T::OFF_Q), "the partial rows fit into the ring");
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -560,6 +595,8 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
           }
         }
       bar();
+      // kCluster: this CTA's sum of each head, behind the warps' rows
+      float* sums = ring + NCW * 8 * NT * kRow;
       for (int h = warp; h < G; h += NCW) {  // a warp a head, a lane 4 channels
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -569,6 +606,11 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         }
         float M, L;
         head_of(h, M, L);
+        if constexpr (kCluster) {
+          *reinterpret_cast<float4*>(sums + h * kRow + 4 * lane) = x;
+          if (lane == 0) *reinterpret_cast<float2*>(sums + h * kRow + 128) = make_float2(M, L);
+          continue;
+        }
         if (whole) {
           const float inv = L == 0.f ? 0.f : kSumUnit / L;
           const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
@@ -581,6 +623,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
       }
       return;
     }
+    if constexpr (kCluster) return;  // a CTA has one segment
     float4* scr = reinterpret_cast<float4*>(smem + T::OFF_SCR);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -643,7 +686,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     bar();  // scratch and (m, l) may be written again
   };
 
-  load_query();
+  if (!kCluster || u1 > u0) load_query();
   const int rbase = 16 * warp;
   const int n_units = u1 - u0;
   int seg_first = u0 - cur.s;  // the segment's first unit (it may lie in an earlier run)
@@ -805,7 +848,49 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
       ++cur.s;
     }
   }
-  clear_empty<kSparse>(p, NCW * 32);
+  if constexpr (!kCluster) {
+    clear_empty<kSparse>(p, NCW * 32);
+  } else {
+    // Each head by one warp of the cluster, from the sums of the CTAs that had
+    // units, in the order of their ranks.
+    cluster_sync();
+    constexpr int kRow = 132;
+    const uint32_t sums = smem_addr(reinterpret_cast<float*>(smem) + NCW * 8 * NT * kRow);
+    const int n = min(static_cast<int>(csize), cur.nst);
+    for (int h = static_cast<int>(rank) * NCW + warp; h < G; h += static_cast<int>(csize) * NCW) {
+      const uint32_t row = sums + static_cast<uint32_t>(h * kRow * 4);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < n) {
+        const uint32_t at = peer_addr(row + 128 * 4, lane);
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(at) : "memory");
+      }
+      float M = ml.x;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+      const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - M);  // no row: zeros, or a NaN
+      float L = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int r = 0; r < n; ++r) {
+        float4 y;
+        const uint32_t at = peer_addr(row + 16 * lane, r);
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                     : "r"(at)
+                     : "memory");
+        const float f = __shfl_sync(0xffffffffu, w, r);
+        L += f * __shfl_sync(0xffffffffu, ml.y, r);
+        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+      }
+      const float inv = L == 0.f ? 0.f : kSumUnit / L;
+      const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
+      *reinterpret_cast<uint2*>(p.out + head * 128 + 4 * lane) =
+          make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+      if (p.lse && lane == 0)
+        p.lse[head] = L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  }
 }
 
 // Merges the partial results of the runs that share a (sequence, KV head), in

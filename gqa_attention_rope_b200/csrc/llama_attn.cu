@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "llama_attn.h"
@@ -260,12 +261,14 @@ int device_setup(int dev, int* n_sm) {
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<false>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<true>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::q8::qkv_fp8_rope_kernel), la::q8::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, false>), la::dpg::Tile<true, false>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, false, true>), la::dpg::Tile<true, true>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, false>), la::dpg::Tile<true, false>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<true, true, true>), la::dpg::Tile<true, true>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, false>), la::dpg::Tile<false, false>::SMEM_ALLOC);
-    attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<false, true, true>), la::dpg::Tile<false, true>::SMEM_ALLOC);
+    auto runs = [&](auto e4m3, auto sparse, auto wide) {
+      constexpr bool E = decltype(e4m3)::value, S = decltype(sparse)::value, W = decltype(wide)::value;
+      attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<E, S, W, false>), la::dpg::Tile<E, W>::SMEM_ALLOC);
+      attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<E, S, W, true>), la::dpg::Tile<E, W>::SMEM_ALLOC);
+    };
+    const std::true_type yes{};
+    const std::false_type no{};
+    runs(yes, no, no), runs(yes, no, yes), runs(yes, yes, no), runs(yes, yes, yes), runs(no, yes, no), runs(no, yes, yes);
     attr(reinterpret_cast<const void*>(la::pap::kv_append_paged_kernel<true, 256, 8>), 256 * 8 * 32);
     attr(reinterpret_cast<const void*>(la::sel::select_blocks_kernel), la::sel::MAX_BLOCKS * 8);
     int n = 0;
@@ -1124,14 +1127,30 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   const int resident = n_sm * (G > 8 ? la::dpg::Tile<kE4M3, true>::CTAS : la::dpg::Tile<kE4M3, false>::CTAS);
   const int grid = resident < la::dpg::MAX_CTAS ? resident : la::dpg::MAX_CTAS;
   std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
-  prof_count(2);
-  const int pair = prof_before(stream);
   using Wide = la::dpg::Tile<kE4M3, true>;
   using Narrow = la::dpg::Tile<kE4M3, false>;
+  // Few pairs of few stages: a cluster per pair
+  const int64_t pairs = static_cast<int64_t>(a.B) * a.Hkv;
+  const int64_t stages = static_cast<int64_t>(kSparse && a.n_sel < a.max_blocks ? a.n_sel : a.max_blocks) *
+                         (a.page_size / la::dpg::ROWS);  // of a pair at most
+  if (pairs * 8 <= resident && stages <= 8 * 16) {
+    prof_count(1);
+    const int pair = prof_before(stream);
+    const dim3 clusters(static_cast<unsigned>(pairs * 8));
+    const cudaError_t e =
+        G > 8 ? launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, true, true>, clusters, Wide::NTHREADS,
+                                 Wide::SMEM_ALLOC, stream, 8, tk, tv, p)
+              : launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, false, true>, clusters, Narrow::NTHREADS,
+                                 Narrow::SMEM_ALLOC, stream, 8, tk, tv, p);
+    prof_after(pair, stream);
+    return cuda_status(e);
+  }
+  prof_count(2);
+  const int pair = prof_before(stream);
   const cudaError_t e =
-      G > 8 ? launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, true>, dim3(grid), Wide::NTHREADS,
+      G > 8 ? launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, true, false>, dim3(grid), Wide::NTHREADS,
                                Wide::SMEM_ALLOC, stream, 1, tk, tv, p)
-            : launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, false>, dim3(grid), Narrow::NTHREADS,
+            : launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, false, false>, dim3(grid), Narrow::NTHREADS,
                                Narrow::SMEM_ALLOC, stream, 1, tk, tv, p);
   prof_after(pair, stream);
   if (e != cudaSuccess) return LLAMA_ATTN_ERR_CUDA;

@@ -327,6 +327,10 @@ DECODE = [
     (64, 32, 2, [2049, 1, 63], 0, 0),
     (64, 13, 13, [90, 200], 0, 0),
     (128, 16, 1, [20000], 1, 0),
+    # more pairs than clusters fit, and caches too long for one: runs over the batch, joined behind
+    (64, 24, 8, [0, 1, 64, 65, 777, 2049, 3, 640], 2, 0),
+    (64, 96, 8, [700, 1, 130, 2000, 64, 0], 0, -1),
+    (64, 3, 1, [9000, 1, 17000], 0, 0),
 ]
 
 
@@ -409,6 +413,13 @@ SPARSE = [
     ("e4m3", 192, 12, 12, [1000, 10], 40, 1, 1, -1),
     ("e4m3", 64, 16, 1, [70001], 128, 4, 4, 0),
     ("bf16", 64, 4, 4, [20011, 9000], 33, 1, 0, 0),
+    # runs over the batch
+    ("bf16", 64, 24, 8, [0, 1, 64, 65, 777, 2049, 3, 640], 7, 1, 1, 0),
+    ("e4m3", 64, 24, 8, [0, 1, 64, 65, 777, 2049, 3, 640], 7, 1, 1, 0),
+    ("bf16", 128, 96, 8, [700, 1, 1300, 2000, 64, 0], 5, 0, 1, -1),
+    ("e4m3", 128, 96, 8, [700, 1, 1300, 2000, 64, 0], 5, 0, 1, -1),
+    ("bf16", 64, 6, 2, [20011, 9000, 100], 180, 1, 1, 0),
+    ("bf16", 64, 24, 2, [20011, 9000, 100], 180, 1, 1, 0),
 ]
 
 
