@@ -31,8 +31,12 @@
 //
 // Work split: a unit is one 64-row stage of one (sequence, KV head). All units
 // of the batch in the order (sequence, head, stage) are cut into gridDim.x
-// equal runs, so ragged lengths leave no CTA idle and the ring of stages never
-// drains between sequences. A (sequence, head) inside one run is written to
+// runs of equal cost, so ragged lengths leave no CTA idle and the ring of
+// stages never drains between sequences. A unit costs 1, and each (sequence,
+// head) PAIR_COST more ahead of its first one: its query, and the join of the
+// warps. 64 sequences of 1 to 4000 rows (log-uniform), 8 KV heads, with 0, 3, 6
+// and 10 for that: 67, 53, 51 and 52 us; 40 sequences of 1 to 1000: 27, 16, 16
+// and 16; equal lengths the same with each. A (sequence, head) inside one run is written to
 // the output directly; one that spans several leaves partial results (at most
 // two per CTA: its first and its last), which decode_join_kernel merges in
 // the order of the runs: the result does not depend on timing.
@@ -52,6 +56,7 @@ constexpr float kLift = 7.f;              // P of the greatest row: 2^7
 // Denominators are kept in units of 2^18: with value scales down to 2^-100 a sum
 // of P / vs over 2^30 rows, P up to 2^15, stays below 2^128.
 constexpr float kSumUnit = 0x1p-18f, kSumUnitLog2 = 18.f;
+constexpr int PAIR_COST = 6;              // a pair's begin and end, in units
 constexpr int MAX_CTAS = 512;             // runs (and twice as many partial results) the workspace holds
 
 // kWide: more than 8 query heads per KV head, two tiles of 8 (NT). Four compute
@@ -103,7 +108,7 @@ struct Params {
   float* lse;                 // [B, Hq] or null
   float* part_o;              // [2 * MAX_CTAS][G][128]
   float2* part_ml;            // [2 * MAX_CTAS][G]
-  int* prefix;                // [B + 1] units before each sequence
+  int* prefix;                // [B + 1] cost before each sequence
   int4* ends;                 // [MAX_CTAS] (sequence, KV head, first run) of a pair that ends in a run but began before
   unsigned int epoch;
 };
@@ -121,6 +126,9 @@ __device__ __forceinline__ int stages_of(const Params& p, int b) {
   }
   return ceil_div(len, ROWS);
 }
+
+// Cost of a pair of that many stages: what its begin and end take, then a unit per stage.
+__device__ __forceinline__ int cost_of(int nst) { return nst > 0 ? nst + PAIR_COST : 0; }
 
 // Position of a unit in the order (sequence, KV head, stage).
 struct Cursor {
@@ -225,6 +233,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
   grid_dependency_wait();
   Cut cut(1, 1);
   int u0 = 0, u1 = 0;  // this CTA's units
+  int first_cost = 0;  // of the first unit of the pair that this CTA begins in
   Cursor cur;
   const uint32_t rank = kCluster ? cluster_rank() : 0u, csize = kCluster ? cluster_size() : 1u;
   if constexpr (kCluster) {
@@ -250,27 +259,32 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     cur.s = u0;
   } else {
     __shared__ int4 s_start;
-    __shared__ int s_part[NTHREADS];
-    // Units before this thread's share of the sequences, and in all: thread i
-    // takes sequences [i * per, (i + 1) * per).
+    __shared__ int3 s_range;  // first and last unit, cost of the first pair's first unit
+    __shared__ int2 s_part[NTHREADS];
+    // Cost and units before this thread's share of the sequences, and the cost
+    // in all: thread i takes sequences [i * per, (i + 1) * per).
     const int per = (p.B + NTHREADS - 1) / NTHREADS;
     const int my0 = min(p.B, static_cast<int>(threadIdx.x) * per), my1 = min(p.B, my0 + per);
     {
-      int sum = 0;
-      for (int b = my0; b < my1; ++b) sum += stages_of<kSparse>(p, b) * p.Hkv;
+      int2 sum = make_int2(0, 0);
+      for (int b = my0; b < my1; ++b) {
+        const int nst = stages_of<kSparse>(p, b);
+        sum.x += cost_of(nst) * p.Hkv, sum.y += nst * p.Hkv;
+      }
       s_part[threadIdx.x] = sum;
     }
     __syncthreads();
-    int before = 0, total = 0;
+    int2 before = make_int2(0, 0);
+    int total = 0, units = 0;
     for (int i = 0; i < NTHREADS && i * per < p.B; ++i) {
-      if (i == static_cast<int>(threadIdx.x)) before = total;
-      total += s_part[i];
+      if (i == static_cast<int>(threadIdx.x)) before = make_int2(total, units);
+      total += s_part[i].x, units += s_part[i].y;
     }
     if (my0 < p.B && blockIdx.x == 0) {  // the joining kernel reads these
-      int at = before;
+      int at = before.x;
       for (int b = my0; b < my1; ++b) {
         p.prefix[b] = at;
-        at += stages_of<kSparse>(p, b) * p.Hkv;
+        at += cost_of(stages_of<kSparse>(p, b)) * p.Hkv;
       }
       if (my1 == p.B) p.prefix[p.B] = at;
     }
@@ -281,21 +295,34 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
       return;
     }
     cut = Cut(total, n_runs);
-    u0 = cut.start(blockIdx.x);
-    u1 = cut.start(blockIdx.x + 1);
-    if (my0 < my1 && before <= u0 && u0 < before + s_part[threadIdx.x]) {  // one thread finds the start
-      int at = before;
-      for (int b = my0; b < my1; ++b) {
-        const int nst = stages_of<kSparse>(p, b), n = nst * p.Hkv;
-        if (u0 < at + n) {
-          const int g = (u0 - at) / nst;
-          s_start = make_int4(b, g, u0 - at - g * nst, nst);
+    const int c0 = cut.start(blockIdx.x), c1 = cut.start(blockIdx.x + 1) - 1;  // first and last cost
+    if (my0 < my1) {  // one thread finds the start, one the end
+      int at = before.x, u = before.y;
+      const int end = at + s_part[threadIdx.x].x;
+      for (int b = my0; b < my1 && at <= c1 && c0 < end; ++b) {
+        const int nst = stages_of<kSparse>(p, b), cost = cost_of(nst), n = cost * p.Hkv;
+        if (at <= c0 && c0 < at + n) {
+          const int g = (c0 - at) / cost, off = c0 - at - g * cost;
+          s_start = make_int4(b, g, max(0, off - PAIR_COST), nst);
+          s_range.x = u + g * nst + max(0, off - PAIR_COST);
+          s_range.z = c0 - off + PAIR_COST;
+        }
+        if (c1 < at + n) {
+          const int g = (c1 - at) / cost, off = c1 - at - g * cost;
+          s_range.y = u + g * nst + max(0, off + 1 - PAIR_COST);
           break;
         }
-        at += n;
+        at += n, u += nst * p.Hkv;
       }
     }
     __syncthreads();
+    u0 = s_range.x;
+    u1 = s_range.y;
+    first_cost = s_range.z;
+    if (u0 == u1) {  // costs of no unit
+      clear_empty<kSparse>(p, NTHREADS);
+      return;
+    }
     cur = Cursor{s_start.x, s_start.y, s_start.z, s_start.w};
   }
 
@@ -542,7 +569,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
     if (!kCluster && first_unit < u0 && last_unit <= u1 && threadIdx.x == 0)
-      p.ends[blockIdx.x] = make_int4(cur.b, cur.g, cut.run_of(first_unit), 0);
+      p.ends[blockIdx.x] = make_int4(cur.b, cur.g, cut.run_of(first_cost), 0);
     // A head's denominator and reference over the four warps, and this warp's factor.
     auto head_of = [&](int h, float& M, float& L) {
       float2 v[NCW];
@@ -973,8 +1000,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
     const int total = p.prefix[p.B], first = p.prefix[b], end = p.prefix[b + 1];
     if (end == first) return;
     const Cut cut(total, min(max_runs, total));
-    const int nst = (end - first) / p.Hkv;
-    const int c0 = cut.run_of(first + g * nst), c1 = cut.run_of(first + (g + 1) * nst - 1);
+    const int cost = (end - first) / p.Hkv;
+    const int c0 = cut.run_of(first + g * cost + PAIR_COST), c1 = cut.run_of(first + (g + 1) * cost - 1);
     if (c0 == c1) return;
     auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
     float M, L;

@@ -1077,8 +1077,9 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   if (kSparse && a.n_sel <= 0) return LLAMA_ATTN_ERR_INVALID_ARG;
   if (a.q_pos_offset != 0 && a.q_pos_offset != -1) return LLAMA_ATTN_ERR_INVALID_ARG;
   if ((st = check_pages(a.B, a.Hkv, a.D, a.page_size, a.max_blocks, a.n_pages))) return st;
-  if (static_cast<int64_t>(a.B) * a.Hkv * a.max_blocks > INT32_MAX / (a.page_size / la::dpg::ROWS))
-    return LLAMA_ATTN_ERR_UNSUPPORTED;  // stages of all sequences and heads are counted in 32 bits
+  if (static_cast<int64_t>(a.B) * a.Hkv >
+      INT32_MAX / (static_cast<int64_t>(a.max_blocks) * (a.page_size / la::dpg::ROWS) + la::dpg::PAIR_COST))
+    return LLAMA_ATTN_ERR_UNSUPPORTED;  // the cost of all sequences and heads is counted in 32 bits
   const size_t rows_bytes = static_cast<size_t>(a.B) * a.Hq * 256;
   if (ranges_overlap(a.out, rows_bytes, a.q, rows_bytes)) return LLAMA_ATTN_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(a.lse) & 3u) return LLAMA_ATTN_ERR_INVALID_ARG;
