@@ -50,6 +50,7 @@ struct DeviceSetup {
   std::once_flag once;
   int status = 0;
   int n_sm = 148;
+  int clusters[la::dpg::MAX_CLUSTER + 1] = {};  // of each size, of the paged decode kernels, that are resident at once
 };
 
 std::mutex g_mutex;
@@ -261,10 +262,35 @@ int device_setup(int dev, int* n_sm) {
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<false>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::dec::decode_split_kernel<true>), la::dec::SMEM_ALLOC);
     attr(reinterpret_cast<const void*>(la::q8::qkv_fp8_rope_kernel), la::q8::SMEM_ALLOC);
+    bool first = true;
     auto runs = [&](auto e4m3, auto sparse, auto wide) {
       constexpr bool E = decltype(e4m3)::value, S = decltype(sparse)::value, W = decltype(wide)::value;
       attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<E, S, W, false>), la::dpg::Tile<E, W>::SMEM_ALLOC);
-      attr(reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<E, S, W, true>), la::dpg::Tile<E, W>::SMEM_ALLOC);
+      using T = la::dpg::Tile<E, W>;
+      const void* fn = reinterpret_cast<const void*>(la::dpg::decode_runs_kernel<E, S, W, true>);
+      attr(fn, T::SMEM_ALLOC);
+      if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        st = LLAMA_ATTN_ERR_CUDA;
+      for (int c = 1; c <= la::dpg::MAX_CLUSTER; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(c);
+        cfg.blockDim = dim3(T::NTHREADS);
+        cfg.dynamicSmemBytes = T::SMEM_ALLOC;
+        cudaLaunchAttribute shape;
+        shape.id = cudaLaunchAttributeClusterDimension;
+        shape.val.clusterDim.x = c;
+        shape.val.clusterDim.y = shape.val.clusterDim.z = 1;
+        cfg.attrs = &shape;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) != cudaSuccess) {
+          cudaGetLastError();  // no cluster of this size on this device: the other form runs
+          fit = 0;
+        }
+        int& n = ds.clusters[c];
+        n = first || fit < n ? fit : n;
+      }
+      first = false;
     };
     const std::true_type yes{};
     const std::false_type no{};
@@ -1130,19 +1156,31 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_mutex);  // only the benchmark instrumentation is shared
   using Wide = la::dpg::Tile<kE4M3, true>;
   using Narrow = la::dpg::Tile<kE4M3, false>;
-  // Few pairs of few stages: a cluster per pair
+  // A cluster per pair where the pairs fit on the device at once and are short:
+  // no second kernel, no run with more than one pair. Its size is the largest of
+  // which all are resident, above 8 from 32 stages on. Clusters and runs, 8 KV
+  // heads: one sequence of 1000 rows 5.5 and 7.8 us (16 CTAs per pair: 6.2), of
+  // 4000 7.8 and 9.0 (8 CTAs: 8.4), of 12000 12.0 and 11.5; 10 of 2000 (3 CTAs)
+  // 11.5 and 12.6; 32 of 250 (1 CTA) 6.7 and 11.0. Lengths of a batch may be far
+  // below the table's: the longest then waits for its own CTAs alone. From 16
+  // stages per CTA on that costs as much as is won (8 of 4000 rows 16.3 and 18.8
+  // us, of 1 to 4000 13.2 and 11.7; of 1 to 2000 9.0 and 9.7). Chosen blocks
+  // are mostly as many for each sequence: 16 of 64 blocks of 64 rows, 64 heads,
+  // 64.0 and 68.0 us with the choice.
   const int64_t pairs = static_cast<int64_t>(a.B) * a.Hkv;
   const int64_t stages = static_cast<int64_t>(kSparse && a.n_sel < a.max_blocks ? a.n_sel : a.max_blocks) *
                          (a.page_size / la::dpg::ROWS);  // of a pair at most
-  if (pairs * 8 <= resident && stages <= 8 * 16) {
+  int csize = stages > 32 ? la::dpg::MAX_CLUSTER : 8;
+  while (csize > 0 && g_setup[dev].clusters[csize] < pairs) --csize;
+  if (stages <= static_cast<int64_t>(csize) * (kSparse ? 32 : 10)) {
     prof_count(1);
     const int pair = prof_before(stream);
-    const dim3 clusters(static_cast<unsigned>(pairs * 8));
+    const dim3 clusters(static_cast<unsigned>(pairs * csize));
     const cudaError_t e =
         G > 8 ? launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, true, true>, clusters, Wide::NTHREADS,
-                                 Wide::SMEM_ALLOC, stream, 8, tk, tv, p)
+                                 Wide::SMEM_ALLOC, stream, csize, tk, tv, p)
               : launch_dependent(la::dpg::decode_runs_kernel<kE4M3, kSparse, false, true>, clusters, Narrow::NTHREADS,
-                                 Narrow::SMEM_ALLOC, stream, 8, tk, tv, p);
+                                 Narrow::SMEM_ALLOC, stream, csize, tk, tv, p);
     prof_after(pair, stream);
     return cuda_status(e);
   }

@@ -327,10 +327,17 @@ DECODE = [
     (64, 32, 2, [2049, 1, 63], 0, 0),
     (64, 13, 13, [90, 200], 0, 0),
     (128, 16, 1, [20000], 1, 0),
-    # more pairs than clusters fit, and caches too long for one: runs over the batch, joined behind
+    # more pairs than clusters of 8 fit, and caches too long for one
     (64, 24, 8, [0, 1, 64, 65, 777, 2049, 3, 640], 2, 0),
     (64, 96, 8, [700, 1, 130, 2000, 64, 0], 0, -1),
     (64, 3, 1, [9000, 1, 17000], 0, 0),
+    # clusters of 1, 3 and 16; more pairs than CTAs are resident, most of a stage or none
+    (64, 8, 8, [5, 0, 64, 130, 1, 640, 65, 31, 200, 128, 0, 2, 63, 400, 66, 7, 500, 1, 129, 64, 30, 3, 0, 90], 1, 0),
+    (64, 16, 8, [600, 0, 1, 64, 65, 129, 300, 2, 1900, 63], 0, -1),
+    (64, 15, 1, [10000, 40], 2, 0),
+    (64, 12, 1, [10000, 0, 64, 65], 0, 0),
+    (64, 8, 8, [(7 * i * i) % 97 if i % 9 else 70 * i for i in range(64)], 3, 0),
+    (128, 40, 4, [1, 0, 2, 700, 1, 1, 130, 1] * 12, 0, 0),
 ]
 
 
@@ -413,13 +420,17 @@ SPARSE = [
     ("e4m3", 192, 12, 12, [1000, 10], 40, 1, 1, -1),
     ("e4m3", 64, 16, 1, [70001], 128, 4, 4, 0),
     ("bf16", 64, 4, 4, [20011, 9000], 33, 1, 0, 0),
-    # runs over the batch
     ("bf16", 64, 24, 8, [0, 1, 64, 65, 777, 2049, 3, 640], 7, 1, 1, 0),
     ("e4m3", 64, 24, 8, [0, 1, 64, 65, 777, 2049, 3, 640], 7, 1, 1, 0),
     ("bf16", 128, 96, 8, [700, 1, 1300, 2000, 64, 0], 5, 0, 1, -1),
     ("e4m3", 128, 96, 8, [700, 1, 1300, 2000, 64, 0], 5, 0, 1, -1),
     ("bf16", 64, 6, 2, [20011, 9000, 100], 180, 1, 1, 0),
     ("bf16", 64, 24, 2, [20011, 9000, 100], 180, 1, 1, 0),
+    # runs over the batch
+    ("bf16", 64, 16, 8, [0, 1, 64, 65, 777, 2049, 3, 640] * 6, 7, 1, 1, 0),
+    ("e4m3", 64, 16, 8, [0, 1, 64, 65, 777, 2049, 3, 640] * 6, 7, 1, 1, 0),
+    ("bf16", 64, 6, 2, [40000, 9000, 100], 560, 1, 1, 0),
+    ("e4m3", 64, 24, 2, [40000, 9000, 100], 560, 1, 1, 0),
 ]
 
 
