@@ -1,6 +1,6 @@
 // decode_paged.cuh -- single-token GQA decode over a paged cache of E4M3 codes
 // with a scale per (page, KV head), and over chosen blocks of a paged cache
-// (E4M3 or bf16): the work of the whole batch is cut into equal runs, one per
+// (E4M3 or bf16): the work of the whole batch is cut into runs of equal cost, one per
 // resident CTA.
 //
 // Mathematics, for the query heads h of a KV group and the cache rows n that
