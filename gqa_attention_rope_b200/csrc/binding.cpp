@@ -116,6 +116,21 @@ cudaStream_t stream_of(Args& a, int device) {
   return static_cast<cudaStream_t>(p);
 }
 
+// The interpreter's lock, given up while this lives and taken back however the scope is left.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+// Calls the library on the tensors' device without the interpreter's lock. The
+// arguments are pointers and sizes by then: forming them may throw (a tensor of
+// a function transform has no storage) and needs the lock.
+template <typename Fn, typename... A>
+int run(int device, Fn fn, A... args) {
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+  const Unlocked unlocked;
+  return fn(args...);
+}
+
 // A page pool and, for E4M3, its scales.
 struct Pool {
   const at::Tensor *k, *v, *ks = nullptr, *vs = nullptr;
@@ -194,23 +209,15 @@ int append(Args& a) {
   const at::Tensor* out_lens = a.tensor_or_none("out_lens");
   if (out_lens) check("out_lens", *out_lens, at::kInt, {B}, device);
   const cudaStream_t stream = stream_of(a, device);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
-  int st;
-  Py_BEGIN_ALLOW_THREADS
   if (e4m3)
-    st = reinterpret_cast<AppendE4m3>(fn)(
-        data<llama_attn_bf16>(k), data<llama_attn_bf16>(v), row, batch, data<uint8_t>(*p.k), data<uint8_t>(*p.v),
-        data<float>(*p.ks), data<float>(*p.vs), data<llama_attn_bf16>(bounds), data<int32_t>(table),
-        data<int32_t>(lens), data<int32_t>(new_lens), data<int32_t>(out_lens), B, T, H, D, p.page_size, blocks,
-        p.n_pages, data<void>(rope), rows, stream);
-  else
-    st = reinterpret_cast<AppendBf16>(fn)(
-        data<llama_attn_bf16>(k), data<llama_attn_bf16>(v), row, batch, data<llama_attn_bf16>(*p.k),
-        data<llama_attn_bf16>(*p.v), data<llama_attn_bf16>(bounds), data<int32_t>(table), data<int32_t>(lens),
-        data<int32_t>(new_lens), data<int32_t>(out_lens), B, T, H, D, p.page_size, blocks, p.n_pages, data<void>(rope),
-        rows, stream);
-  Py_END_ALLOW_THREADS
-  return st;
+    return run(device, reinterpret_cast<AppendE4m3>(fn), data<llama_attn_bf16>(k), data<llama_attn_bf16>(v), row, batch,
+               data<uint8_t>(*p.k), data<uint8_t>(*p.v), data<float>(*p.ks), data<float>(*p.vs),
+               data<llama_attn_bf16>(bounds), data<int32_t>(table), data<int32_t>(lens), data<int32_t>(new_lens),
+               data<int32_t>(out_lens), B, T, H, D, p.page_size, blocks, p.n_pages, data<void>(rope), rows, stream);
+  return run(device, reinterpret_cast<AppendBf16>(fn), data<llama_attn_bf16>(k), data<llama_attn_bf16>(v), row, batch,
+             data<llama_attn_bf16>(*p.k), data<llama_attn_bf16>(*p.v), data<llama_attn_bf16>(bounds),
+             data<int32_t>(table), data<int32_t>(lens), data<int32_t>(new_lens), data<int32_t>(out_lens), B, T, H, D,
+             p.page_size, blocks, p.n_pages, data<void>(rope), rows, stream);
 }
 
 // (function, e4m3, q, kpages, vpages[, k_scales, v_scales], block_table,
@@ -248,26 +255,20 @@ int decode(Args& a) {
   const int offset = a.integer("q_pos_offset");
   const float theta = a.real();
   const cudaStream_t stream = stream_of(a, device);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
-  int st;
-  Py_BEGIN_ALLOW_THREADS
   if (!ids)
-    st = reinterpret_cast<DecodeE4m3>(fn)(
-        data<llama_attn_bf16>(q), data<uint8_t>(*p.k), data<uint8_t>(*p.v), data<float>(*p.ks), data<float>(*p.vs),
-        data<int32_t>(table), data<int32_t>(lens), data<llama_attn_bf16>(out), data<float>(lse), B, Hq, p.heads, D,
-        p.page_size, blocks, p.n_pages, offset, theta, data<void>(ws), ws.nbytes(), stream);
-  else if (e4m3)
-    st = reinterpret_cast<SparseE4m3>(fn)(
-        data<llama_attn_bf16>(q), data<uint8_t>(*p.k), data<uint8_t>(*p.v), data<float>(*p.ks), data<float>(*p.vs),
-        data<int32_t>(table), data<int32_t>(*ids), data<int32_t>(lens), data<llama_attn_bf16>(out), data<float>(lse), B,
-        Hq, p.heads, D, p.page_size, blocks, p.n_pages, n_sel, offset, theta, data<void>(ws), ws.nbytes(), stream);
-  else
-    st = reinterpret_cast<SparseBf16>(fn)(
-        data<llama_attn_bf16>(q), data<llama_attn_bf16>(*p.k), data<llama_attn_bf16>(*p.v), data<int32_t>(table),
-        data<int32_t>(*ids), data<int32_t>(lens), data<llama_attn_bf16>(out), data<float>(lse), B, Hq, p.heads, D,
-        p.page_size, blocks, p.n_pages, n_sel, offset, theta, data<void>(ws), ws.nbytes(), stream);
-  Py_END_ALLOW_THREADS
-  return st;
+    return run(device, reinterpret_cast<DecodeE4m3>(fn), data<llama_attn_bf16>(q), data<uint8_t>(*p.k),
+               data<uint8_t>(*p.v), data<float>(*p.ks), data<float>(*p.vs), data<int32_t>(table), data<int32_t>(lens),
+               data<llama_attn_bf16>(out), data<float>(lse), B, Hq, p.heads, D, p.page_size, blocks, p.n_pages, offset,
+               theta, data<void>(ws), ws.nbytes(), stream);
+  if (e4m3)
+    return run(device, reinterpret_cast<SparseE4m3>(fn), data<llama_attn_bf16>(q), data<uint8_t>(*p.k),
+               data<uint8_t>(*p.v), data<float>(*p.ks), data<float>(*p.vs), data<int32_t>(table), data<int32_t>(*ids),
+               data<int32_t>(lens), data<llama_attn_bf16>(out), data<float>(lse), B, Hq, p.heads, D, p.page_size, blocks,
+               p.n_pages, n_sel, offset, theta, data<void>(ws), ws.nbytes(), stream);
+  return run(device, reinterpret_cast<SparseBf16>(fn), data<llama_attn_bf16>(q), data<llama_attn_bf16>(*p.k),
+             data<llama_attn_bf16>(*p.v), data<int32_t>(table), data<int32_t>(*ids), data<int32_t>(lens),
+             data<llama_attn_bf16>(out), data<float>(lse), B, Hq, p.heads, D, p.page_size, blocks, p.n_pages, n_sel,
+             offset, theta, data<void>(ws), ws.nbytes(), stream);
 }
 
 // (function, q, kbounds, block_table, cache_lens, block_ids, page_size, n_sel,
@@ -295,13 +296,9 @@ int select(Args& a) {
   check("block_ids", ids, at::kInt, {B, H, n_sel}, device);
   const float theta = a.real();
   const cudaStream_t stream = stream_of(a, device);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
-  int st;
-  Py_BEGIN_ALLOW_THREADS
-  st = fn(data<llama_attn_bf16>(q), data<llama_attn_bf16>(bounds), data<int32_t>(table), data<int32_t>(lens),
-          data<int32_t>(ids), B, Hq, H, D, page_size, blocks, n_pages, n_sel, n_first, n_last, offset, theta, stream);
-  Py_END_ALLOW_THREADS
-  return st;
+  return run(device, fn, data<llama_attn_bf16>(q), data<llama_attn_bf16>(bounds), data<int32_t>(table),
+             data<int32_t>(lens), data<int32_t>(ids), B, Hq, H, D, page_size, blocks, n_pages, n_sel, n_first, n_last,
+             offset, theta, stream);
 }
 
 template <int (*kCall)(Args&)>

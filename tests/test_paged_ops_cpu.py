@@ -4,6 +4,7 @@ would return LLAMA_ATTN_ERR_CUDA instead), the binding's own checks, and the
 float64 statements the GPU tests compare with."""
 import ctypes
 import math
+import types
 
 import pytest
 import torch
@@ -148,6 +149,53 @@ def test_binding_fails_loudly_when_it_is_not_built(lib, monkeypatch, tmp_path):
     monkeypatch.setattr(la, "_PKG", str(tmp_path))
     with pytest.raises(RuntimeError, match="_binding.so not found"):
         la._native()
+
+
+def fake_cuda_call():
+    """Arguments that pass every check of the binding on a host without a GPU: tensors that say they are on cuda:0,
+    and a stream object. Nothing of them is ever read."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    with FakeTensorMode():
+        def e(*shape, dtype=torch.bfloat16):
+            return torch.empty(*shape, dtype=dtype, device="cuda:0")
+        table, lens = e(2, 2, dtype=i32), e(2, dtype=i32)
+        stream = types.SimpleNamespace(device_index=0, cuda_stream=0)
+        scales = dict(k_scales=e(5, 2, dtype=f32), v_scales=e(5, 2, dtype=f32))
+        bf16 = dict(kpages=e(5, 2, 64, 128), vpages=e(5, 2, 64, 128))
+        e4m3 = dict(kpages=e(5, 2, 64, 128, dtype=u8), vpages=e(5, 2, 64, 128, dtype=u8), **scales)
+        both = dict(block_table=table, cache_lens=lens, stream=stream)
+        append = dict(k=e(2, 3, 2, 128), v=e(2, 3, 2, 128), rope_table=e(128, 64, 2, dtype=f32),
+                      out_lens=e(2, dtype=i32), **both)
+        decode = dict(q=e(2, 4, 128), out=e(2, 4, 128), workspace=e(1 << 20, dtype=u8), **both)
+        sparse = dict(decode, block_ids=e(2, 2, 3, dtype=i32))
+        select = dict(q=e(2, 4, 128), kbounds=e(5, 2, 2, 128), block_ids=e(2, 2, 3, dtype=i32), page_size=64, n_sel=3,
+                      **both)
+    return [(la.llama_attn_kv_append_paged, dict(append, **bf16)),
+            (la.llama_attn_kv_append_paged_e4m3, dict(append, **e4m3)),
+            (la.llama_attn_decode_paged_e4m3, dict(decode, **e4m3)),
+            (la.llama_attn_decode_paged_sparse, dict(sparse, **bf16)),
+            (la.llama_attn_decode_paged_sparse_e4m3, dict(sparse, **e4m3)),
+            (la.llama_attn_select_blocks, select)]
+
+
+@pytest.mark.parametrize("i", range(6))
+def test_binding_refuses_tensors_without_storage(lib, i):
+    """A tensor of a function transform has no data: refused where the pointers are formed, before
+    the device is switched and the interpreter's lock is given up."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    call, args = fake_cuda_call()[i]
+    for name in ("k", "q", "block_table", "cache_lens"):
+        if name not in args:
+            continue
+        with FakeTensorMode():
+            many = torch.empty(3, *args[name].shape, dtype=args[name].dtype, device="cuda:0")
+
+        def one(x):
+            with pytest.raises(ValueError, match="storage"):
+                call(**{**args, name: x})
+            return x
+        torch.func.vmap(one)(many)
 
 
 # ---- the statements the GPU tests rely on

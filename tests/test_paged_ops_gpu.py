@@ -828,3 +828,20 @@ def test_many_sequences():
     zero = torch.zeros_like(d["lens"])
     out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], zero, lse=lse)
     assert not out.any() and torch.isinf(lse).all()
+
+
+def test_tensors_without_storage_are_refused_and_the_process_goes_on():
+    """Under a function transform the binding gets tensors that have no data: a ValueError, and the next call runs."""
+    s = attention_state("e4m3", 64, 4, 1, [100], 55)
+    d = on_gpu(s)
+    bounds = bounds_of(s).cuda()
+
+    def one(q):
+        with pytest.raises(ValueError, match="storage"):
+            la.llama_attn_select_blocks(q, bounds, d["table"], d["lens"], 64, 1)
+        with pytest.raises(ValueError, match="storage"):
+            la.llama_attn_decode_paged_e4m3(q, *d["pools"], *d["scales"], d["table"], d["lens"])
+        return q
+    torch.func.vmap(one)(d["q"][None].repeat(2, 1, 1, 1))
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"])
+    check_attention("e4m3", out, None, R.decode(s["q"], s["kv"], s["vv"], s["table"], s["lens"], 64, THETA), 7.0, 100)
