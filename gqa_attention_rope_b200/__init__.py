@@ -585,7 +585,8 @@ def llama_attn_decode_runs_workspace_size(B: int, Hq: int, Hkv: int, D: int = 12
     return int(lib().llama_attn_decode_runs_workspace_size(int(B), int(Hq), int(Hkv), int(D)))
 
 
-def _decode_runs(fn, q, pool, block_table, block_ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream):
+def _decode_runs(fn, q, pool, block_table, ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream):
+    """pool: pages, and scales of E4M3 pages; ids: (block_ids,), or () for all rows."""
     module = _module or _native()
     if out is None or workspace is None:
         import torch
@@ -596,8 +597,8 @@ def _decode_runs(fn, q, pool, block_table, block_ids, cache_lens, out, lse, work
         if workspace is None:
             need = llama_attn_decode_runs_workspace_size(q.shape[0], q.shape[1], pool[0].shape[1], q.shape[2])
             workspace = _empty(max(1, need), torch.uint8, q, stream)
-    st = module.decode(_entry[fn], len(pool) == 4, q, *pool, block_table, block_ids, cache_lens, out, lse, workspace,
-                       q_pos_offset, rope_theta, stream)
+    st = module.decode(_entry[fn], len(pool) == 4, len(ids), q, *pool, block_table, *ids, cache_lens, out, lse,
+                       workspace, q_pos_offset, rope_theta, stream)
     if st:
         _check(fn, st)
     return out
@@ -610,7 +611,7 @@ def llama_attn_decode_paged_e4m3(q, kpages, vpages, k_scales, v_scales, block_ta
     rotated at cache_lens[b] + q_pos_offset: 0 as in llama_attn_decode, -1 where
     its own key has been appended. lse float32 [B,Hq] (optional) gets the
     log-sum-exp. Returns out [B,Hq,128]."""
-    return _decode_runs("llama_attn_decode_paged_e4m3", q, (kpages, vpages, k_scales, v_scales), block_table, None,
+    return _decode_runs("llama_attn_decode_paged_e4m3", q, (kpages, vpages, k_scales, v_scales), block_table, (),
                         cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream)
 
 
@@ -640,7 +641,7 @@ def llama_attn_decode_paged_sparse(q, kpages, vpages, block_table, block_ids, ca
     bf16 page pool (ascending, each once, -1 behind the last; as
     llama_attn_select_blocks gives them). Other arguments as for
     llama_attn_decode_paged_e4m3. Returns out [B,Hq,128]."""
-    return _decode_runs("llama_attn_decode_paged_sparse", q, (kpages, vpages), block_table, block_ids, cache_lens, out,
+    return _decode_runs("llama_attn_decode_paged_sparse", q, (kpages, vpages), block_table, (block_ids,), cache_lens, out,
                         lse, workspace, q_pos_offset, rope_theta, stream)
 
 
@@ -649,7 +650,7 @@ def llama_attn_decode_paged_sparse_e4m3(q, kpages, vpages, k_scales, v_scales, b
                                         rope_theta: float = 500000.0, stream=None):
     """llama_attn_decode_paged_sparse over an E4M3 page pool with its scales."""
     return _decode_runs("llama_attn_decode_paged_sparse_e4m3", q, (kpages, vpages, k_scales, v_scales), block_table,
-                        block_ids, cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream)
+                        (block_ids,), cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream)
 
 
 def shard_units(n_units: int, world_size: int, rank: int):

@@ -220,11 +220,13 @@ int append(Args& a) {
              p.page_size, blocks, p.n_pages, data<void>(rope), rows, stream);
 }
 
-// (function, e4m3, q, kpages, vpages[, k_scales, v_scales], block_table,
-// block_ids or None, cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream)
+// (function, e4m3, sparse, q, kpages, vpages[, k_scales, v_scales], block_table[,
+// block_ids], cache_lens, out, lse, workspace, q_pos_offset, rope_theta, stream);
+// e4m3 and sparse belong to the function: they say which prototype it has.
 int decode(Args& a) {
   void* fn = a.function<void*>();
-  const bool e4m3 = a.integer("e4m3") != 0;
+  const bool e4m3 = a.integer("e4m3") != 0, sparse = a.integer("sparse") != 0;
+  if (!e4m3 && !sparse) throw std::invalid_argument("a decode over E4M3 pages or over chosen blocks expected");
   const at::Tensor& q = a.tensor("q");
   const int device = device_of("q", q);
   check_dims("q", q, 3);
@@ -236,9 +238,9 @@ int decode(Args& a) {
   check_dims("block_table", table, 2);
   const int blocks = dim(table, 1);
   check("block_table", table, at::kInt, {B, blocks}, device);
-  const at::Tensor* ids = a.tensor_or_none("block_ids");
+  const at::Tensor* ids = sparse ? &a.tensor("block_ids") : nullptr;
   int n_sel = 0;
-  if (ids) {
+  if (sparse) {
     check_dims("block_ids", *ids, 3);
     n_sel = dim(*ids, 2);
     check("block_ids", *ids, at::kInt, {B, p.heads, n_sel}, device);
@@ -255,7 +257,7 @@ int decode(Args& a) {
   const int offset = a.integer("q_pos_offset");
   const float theta = a.real();
   const cudaStream_t stream = stream_of(a, device);
-  if (!ids)
+  if (!sparse)
     return run(device, reinterpret_cast<DecodeE4m3>(fn), data<llama_attn_bf16>(q), data<uint8_t>(*p.k),
                data<uint8_t>(*p.v), data<float>(*p.ks), data<float>(*p.vs), data<int32_t>(table), data<int32_t>(lens),
                data<llama_attn_bf16>(out), data<float>(lse), B, Hq, p.heads, D, p.page_size, blocks, p.n_pages, offset,

@@ -198,6 +198,19 @@ def test_binding_refuses_tensors_without_storage(lib, i):
         torch.func.vmap(one)(many)
 
 
+@pytest.mark.parametrize("i", range(6))
+def test_binding_refuses_none_for_every_tensor_it_needs(lib, i):
+    """None is refused by name, not taken for an optional tensor or another call's arguments."""
+    call, args = fake_cuda_call()[i]
+    needed = [n for n, x in args.items() if isinstance(x, torch.Tensor) and n not in ("out_lens", "out", "workspace")]
+    if call is la.llama_attn_select_blocks:
+        needed.remove("block_ids")  # made by the call
+    assert {"block_table", "cache_lens"} < set(needed)
+    for name in needed:
+        with pytest.raises(ValueError, match=f"{name}: tensor expected"):
+            call(**{**args, name: None})
+
+
 # ---- the statements the GPU tests rely on
 def test_reference_grid_is_the_formats():
     from oracle import fp8 as F

@@ -845,3 +845,10 @@ def test_tensors_without_storage_are_refused_and_the_process_goes_on():
     torch.func.vmap(one)(d["q"][None].repeat(2, 1, 1, 1))
     out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"])
     check_attention("e4m3", out, None, R.decode(s["q"], s["kv"], s["vv"], s["table"], s["lens"], 64, THETA), 7.0, 100)
+
+
+def test_sparse_decodes_need_their_block_ids():
+    for kind, fn in (("bf16", la.llama_attn_decode_paged_sparse), ("e4m3", la.llama_attn_decode_paged_sparse_e4m3)):
+        d = on_gpu(attention_state(kind, 64, 4, 1, [100], 57))
+        with pytest.raises(ValueError, match="block_ids: tensor expected"):
+            fn(d["q"], *d["pools"], *d["scales"], d["table"], None, d["lens"])
