@@ -559,7 +559,8 @@ def llama_attn_kv_append_paged(k, v, kpages, vpages, block_table, cache_lens, ro
     with ``rope_table`` (llama_attn_rope_table_build, max_blocks * page_size
     rows). new_lens int32 [B]: rows per sequence where they are fewer than T.
     kbounds bf16 [n_pages,Hkv,2,128]: per block least and greatest key, kept for
-    llama_attn_select_blocks. out_lens int32 [B] gets the new lengths. Returns out_lens."""
+    llama_attn_select_blocks. out_lens int32 [B] gets the new lengths; neither
+    cache_lens nor new_lens may be given for it. Returns out_lens."""
     module = _module or _native()
     st = module.append(_entry["llama_attn_kv_append_paged"], 0, k, v, kpages, vpages, block_table, cache_lens,
                        rope_table, new_lens, kbounds, out_lens, stream)

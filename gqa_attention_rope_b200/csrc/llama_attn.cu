@@ -1018,7 +1018,10 @@ int kv_append_paged(const AppendArgs& a, cudaStream_t stream) {
   if (!aligned16(a.k) || !aligned16(a.v) || !aligned16(a.kpages) || !aligned16(a.vpages) || !aligned16(a.rope_table) ||
       !aligned16(a.kbounds))
     return LLAMA_ATTN_ERR_INVALID_ARG;
-  if (a.out_lens && ranges_overlap(a.out_lens, sizeof(int32_t) * a.B, a.cache_lens, sizeof(int32_t) * a.B))
+  // one CTA of a sequence writes out_lens while others still read these
+  const size_t lens_bytes = sizeof(int32_t) * a.B;
+  if (a.out_lens && (ranges_overlap(a.out_lens, lens_bytes, a.cache_lens, lens_bytes) ||
+                     (a.new_lens && ranges_overlap(a.out_lens, lens_bytes, a.new_lens, lens_bytes))))
     return LLAMA_ATTN_ERR_INVALID_ARG;
   la::pap::Params p;
   p.k = a.k;

@@ -404,8 +404,8 @@ int llama_attn_decode_noalloc(const llama_attn_bf16 *q, const llama_attn_bf16 *k
  *               ([.., 0, :]) and greatest ([.., 1, :]) rotated key of the
  *               block's rows, for llama_attn_select_blocks. A block whose first
  *               row is appended starts anew; otherwise the bounds there widen
- *   out_lens    [B] int32 or NULL: cache_lens[b] + new_lens[b]; must not
- *               overlap cache_lens
+ *   out_lens    [B] int32 or NULL: cache_lens[b] + new_lens[b]; must overlap
+ *               neither cache_lens nor new_lens
  *   rope_table, rope_rows  a table from llama_attn_rope_table_build with at
  *               least max_blocks * page_size rows
  *   T >= 1.

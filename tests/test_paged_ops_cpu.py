@@ -59,6 +59,16 @@ def test_append_refuses(lib, kw, expect):
     assert lib.llama_attn_kv_append_paged_e4m3(*args(list(APPEND), APPEND, kw), None) == expect
 
 
+@pytest.mark.parametrize("off", [0, 4, -4])
+def test_append_refuses_new_lengths_that_it_would_overwrite(lib, off):
+    """out_lens is written by one CTA of a sequence while others still read new_lens."""
+    kw = dict(new=P2, out_lens=ctypes.c_void_p(P2.value + off))
+    order = [n for n in APPEND if n not in ("ks", "vs")]
+    assert lib.llama_attn_kv_append_paged(*args(order, APPEND, kw), None) == INVALID
+    assert lib.llama_attn_kv_append_paged_e4m3(*args(list(APPEND), APPEND, kw), None) == INVALID
+    assert lib.llama_attn_kv_append_paged(*args(order, APPEND, kw), None) not in (INVALID, UNSUPPORTED)
+
+
 def test_append_e4m3_needs_scales(lib):
     for kw in (dict(ks=None), dict(vs=None)):
         assert lib.llama_attn_kv_append_paged_e4m3(*args(list(APPEND), APPEND, kw), None) == INVALID
