@@ -9,7 +9,15 @@
 // with k_n, v_n the codes and ks_n, vs_n the scales of row n's block (1 for
 // bf16). A row's value scale is put into its exponent: P_hn = 2^(s_hn + log2
 // vs_n - m) with m a running bound of the whole exponent, so P stays within
-// range of 16 bits whatever the scales are; the denominator adds P_hn / vs_n.
+// range of 16 bits whatever the scales are. The denominator is a sum of its own:
+// where value scales differ by 2^100 and more, a row may vanish as P and still have
+// most of the weight (a block of zeros, which the append gives the scale 2^-100,
+// next to one of scale 2^40). It adds 2^(s_hn + log2 vs_n - m + d - log2 vs_n), with
+// d such that m - d is a running bound of the scores alone, and the result is
+// O 2^d / L. On bf16 pages all scales are 1, d is 0 and P serves both sums. The
+// second exponential costs two tiles of heads 6% (one 131072-row sequence under
+// 128 heads 55.2 -> 58.6 us) and one tile 1%; forming it only where scales are far
+// apart took more (registers of the rare path spill: 59 to 64 us).
 //
 // What bounds it: HBM. A row of an E4M3 cache is 256 bytes for 4 * 128 * G
 // flop. 64 sequences of 1024 to 32768 rows, 64 heads over 8: 341 us, 6490 GB/s
@@ -56,9 +64,7 @@ namespace dpg {
 constexpr int ROWS = 64;                  // cache rows of a stage
 constexpr int NRW = 4;                    // row groups: 16 rows of a stage each
 constexpr float kLift = 7.f;              // P of the greatest row: 2^7
-// Denominators are kept in units of 2^18: with value scales down to 2^-100 a sum
-// of P / vs over 2^30 rows, P up to 2^15, stays below 2^128.
-constexpr float kSumUnit = 0x1p-18f, kSumUnitLog2 = 18.f;
+constexpr float kSlack = 8.f;             // the bounds move when a row passes them by more: P <= 2^15, weights <= 2^8
 constexpr int PAIR_COST = 6;              // a pair's begin and end, in units
 constexpr int MAX_CLUSTER = 16;
 constexpr int MAX_CTAS = 512;             // runs (and twice as many partial results) the workspace holds
@@ -90,10 +96,11 @@ struct Tile {
   static constexpr uint32_t Q_ROW = 264;                          // bytes: 128 16-bit values, 8 bytes of padding
   static constexpr uint32_t OFF_META = OFF_Q + (kE4M3 || !kWide ? 16 : 32) * Q_ROW;
   static constexpr uint32_t OFF_BAR = OFF_META + NSTAGE * 16;
-  static constexpr uint32_t OFF_ML = OFF_BAR + 128;               // per warp and head: m, l
-  static constexpr uint32_t OFF_CS = OFF_ML + NCW * 16 * 8;       // (cos, sin) row of the segment
+  static constexpr uint32_t OFF_ML = OFF_BAR + 128;               // per warp and head: m, d, l
+  static constexpr uint32_t OFF_CS = OFF_ML + NCW * 16 * 16;      // (cos, sin) row of the segment
   static constexpr uint32_t OFF_QS = OFF_CS + 64 * 8;             // per head: factor of the query row
-  static constexpr uint32_t SMEM_ALLOC = OFF_QS + 64 + 1024;
+  static constexpr uint32_t OFF_D = OFF_QS + 64;                  // per warp and head: d, where it is not in registers
+  static constexpr uint32_t SMEM_ALLOC = OFF_D + NCW * 16 * 4 + 1024;
 };
 
 struct Params {
@@ -111,7 +118,7 @@ struct Params {
   uint16_t* out;              // [B, Hq, 128] bf16
   float* lse;                 // [B, Hq] or null
   float* part_o;              // [2 * MAX_CTAS][G][128]
-  float2* part_ml;            // [2 * MAX_CTAS][G]
+  float4* part_ml;            // [2 * MAX_CTAS][G]: m, d, l
   int* prefix;                // [B + 1] cost before each sequence
   int4* ends;                 // [MAX_CTAS] (sequence, KV head, first run) of a pair that ends in a run but began before
   unsigned int epoch;
@@ -188,6 +195,30 @@ __device__ __forceinline__ uint32_t f16x2_of_hi(uint32_t w) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The greatest of a warp's values (NaN are passed over).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Factor of a sum whose exponents are relative to x where `top` is the greatest
+// such reference; a sum of no row is 0 (or a NaN).
+__device__ __forceinline__ float rebase(float x, float top) { return x == -INFINITY ? 1.f : ex2_approx(x - top); }
+// The unit m - d of a denominator, relative to M (m = -inf: no row).
+__device__ __forceinline__ float unit_of(const float4& v, float M) { return v.x == -INFINITY ? -INFINITY : (v.x - M) - v.y; }
+// From O to the output, 2^d / l, for v = (m, d, l). d lies within [-115, 120] (value
+// scales within [2^-100, 2^119], m behind the greatest exponent by kLift to kLift +
+// kSlack, m - d behind the greatest score by up to kSlack) and l may be as great as
+// 2^39, so neither factor alone leaves float32's range.
+struct Norm {
+  float inv, f;
+  __device__ __forceinline__ explicit Norm(const float4& v) : inv(v.z == 0.f ? 0.f : 1.f / v.z), f(v.z == 0.f ? 0.f : ex2_approx(v.y)) {}
+  __device__ __forceinline__ float operator()(float x) const { return x * inv * f; }
+};
+__device__ __forceinline__ float lse_of(const float4& v) {
+  return v.z == 0.f ? -INFINITY : (v.x + (log2f(v.z) - v.y)) * 0.6931471805599453f;
 }
 
 // Sequences without rows: zeros, dealt out over the CTAs; `n` threads of each.
@@ -435,7 +466,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         const float vs = fminf(fmaxf(__shfl_sync(0xffffffffu, now.vs, j), 7.888609e-31f), 6.646140e35f);
         if (lane == 0 && ok) {
           *reinterpret_cast<float4*>(smem + T::OFF_META + st * 16) =
-              make_float4(__int_as_float(nvalid), ks, kE4M3 ? __log2f(vs) : 0.f, kE4M3 ? kSumUnit / vs : kSumUnit);
+              make_float4(__int_as_float(nvalid), ks, kE4M3 ? __log2f(vs) : 0.f, 0.f);
           if (nvalid > 0)
             mbar_arrive_expect_tx(full(st), T::STAGE);
           else
@@ -468,7 +499,27 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
   const int G = p.G;
   auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(NCW * 32) : "memory"); };
   uint32_t qb[T::Q_REGS ? NQ : 1][T::Q_REGS ? NT : 1][8][2] = {};
-  float qf[NT][2], m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2];
+  // d of a tile's two heads. Two tiles as runs have no registers left for it: one
+  // 131072-row sequence under 128 heads takes 61 us with d in registers and 58.5
+  // with d in shared memory; as clusters seven sequences up to 9001 rows under 16
+  // heads 12.1 and 12.7 us, and a 1000-row sequence under 32 heads 5.5 and 5.7.
+  constexpr bool kRegsD = !kWide || kCluster;
+  float2 d_regs[kRegsD ? NT : 1] = {};
+  float2* const d_smem = reinterpret_cast<float2*>(smem + T::OFF_D + 64 * warp) + t;
+  auto get_d = [&](int nt) {
+    if constexpr (!kE4M3) return make_float2(0.f, 0.f);
+    return kRegsD ? d_regs[kRegsD ? nt : 0] : d_smem[4 * nt];
+  };
+  auto set_d = [&](int nt, float2 x) {  // all lanes of the warp
+    if constexpr (kRegsD) {
+      d_regs[nt] = x;
+    } else {
+      __syncwarp();
+      if (gq == 0) d_smem[4 * nt] = x;
+      __syncwarp();
+    }
+  };
   float o[NT][8][4];
   // B fragment of the query for k step c, from shared memory; q_frag: from where the kernel keeps it.
   auto q_read = [&](int term, int nt, int c, uint32_t& b0, uint32_t& b1) {
@@ -537,10 +588,10 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        qf[nt][e] = kE4M3 ? reinterpret_cast<const float*>(smem + T::OFF_QS)[8 * nt + 2 * t + e] : p.scale_log2;
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
       }
+      if constexpr (kE4M3) set_d(nt, make_float2(0.f, 0.f));
 #pragma unroll
       for (int c = 0; c < 8; ++c)
 #pragma unroll
@@ -558,46 +609,52 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
 
   // Joins the four warps' results of the segment that ends here, and writes it.
   auto finish = [&](int first_unit, int last_unit, bool last) {  // last: of this run
-    float2* ml = reinterpret_cast<float2*>(smem + T::OFF_ML);  // [warp][head]
+    float4* ml = reinterpret_cast<float4*>(smem + T::OFF_ML);  // [warp][head]
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 d = get_d(nt);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float& s = l[nt][e];
         s += __shfl_xor_sync(0xffffffffu, s, 4);
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
-        if (gq == 0) ml[warp * 16 + 8 * nt + 2 * t + e] = make_float2(m[nt][e], s);
+        if (gq == 0) ml[warp * 16 + 8 * nt + 2 * t + e] = make_float4(m[nt][e], e ? d.y : d.x, s, 0.f);
       }
+    }
     bar();
     const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
     if (!kCluster && first_unit < u0 && last_unit <= u1 && threadIdx.x == 0)
       p.ends[blockIdx.x] = make_int4(cur.b, cur.g, cut.run_of(first_cost), 0);
-    // A head's denominator and reference over the four warps, and this warp's factor.
-    auto head_of = [&](int h, float& M, float& L) {
-      float2 v[NCW];
+    // A head's m, and its (m, d, l), over the four warps.
+    auto bound_of = [&](int h) {
+      float M = ml[h].x;
 #pragma unroll
-      for (int w = 0; w < NCW; ++w) v[w] = ml[w * 16 + h];
-      M = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-      L = 0.f;
-#pragma unroll
-      for (int w = 0; w < NCW; ++w) L += v[w].x == -INFINITY ? v[w].y : v[w].y * ex2_approx(v[w].x - M);  // no row: 0 (or a NaN)
+      for (int w = 1; w < NCW; ++w) M = fmaxf(M, ml[w * 16 + h].x);
+      return M;
     };
-    auto store_stats = [&](int h, float M, float L) {
+    auto head_of = [&](int h) {
+      float4 x = make_float4(bound_of(h), 0.f, 0.f, 0.f);
+      float unit[NCW], top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < NCW; ++w) top = fmaxf(top, unit[w] = unit_of(ml[w * 16 + h], x.x));
+#pragma unroll
+      for (int w = 0; w < NCW; ++w) x.z += ml[w * 16 + h].z * rebase(unit[w], top);
+      x.y = -top;
+      return x;
+    };
+    auto store_stats = [&](int h, const float4& v) {
       if (!whole)
-        p.part_ml[slot * G + h] = make_float2(M, L);
+        p.part_ml[slot * G + h] = v;
       else if (p.lse)
-        p.lse[static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h] =
-            L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
+        p.lse[static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h] = lse_of(v);
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float M, L;
-        head_of(8 * nt + 2 * t + e, M, L);
-        const float f = m[nt][e] == -INFINITY ? 1.f : ex2_approx(m[nt][e] - M);
+        const float f = rebase(m[nt][e], bound_of(8 * nt + 2 * t + e));
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           o[nt][c][e] *= f;
@@ -635,22 +692,21 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
           const float4 y = *reinterpret_cast<const float4*>(ring + (w * 8 * NT + h) * kRow + 4 * lane);
           x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
-        float M, L;
-        head_of(h, M, L);
+        const float4 v = head_of(h);
         if constexpr (kCluster) {
           *reinterpret_cast<float4*>(sums + h * kRow + 4 * lane) = x;
-          if (lane == 0) *reinterpret_cast<float2*>(sums + h * kRow + 128) = make_float2(M, L);
+          if (lane == 0) *reinterpret_cast<float4*>(sums + h * kRow + 128) = v;
           continue;
         }
         if (whole) {
-          const float inv = L == 0.f ? 0.f : kSumUnit / L;
+          const Norm norm(v);
           const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
           *reinterpret_cast<uint2*>(p.out + head * 128 + 4 * lane) =
-              make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+              make_uint2(pack_bf16x2(norm(x.x), norm(x.y)), pack_bf16x2(norm(x.z), norm(x.w)));
         } else {
           *reinterpret_cast<float4*>(p.part_o + (slot * G + h) * 128 + 4 * lane) = x;
         }
-        if (lane == 0) store_stats(h, M, L);
+        if (lane == 0) store_stats(h, v);
       }
       return;
     }
@@ -687,21 +743,20 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         for (int e = 0; e < 2; ++e) {
           const int h = 8 * nt + 2 * t + e;
           if (h >= G) continue;
-          float M, L;
-          head_of(h, M, L);
+          const float4 v = head_of(h);
           const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
-          const float inv = L == 0.f ? 0.f : kSumUnit / L;
+          const Norm norm(v);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float x = o[nt][c][e], y = o[nt][c][2 + e];
             if constexpr (kE4M3) {
               if (whole)
-                *reinterpret_cast<uint32_t*>(p.out + head * 128 + 16 * c + 2 * gq) = pack_bf16x2(x * inv, y * inv);
+                *reinterpret_cast<uint32_t*>(p.out + head * 128 + 16 * c + 2 * gq) = pack_bf16x2(norm(x), norm(y));
               else
                 *reinterpret_cast<float2*>(p.part_o + (slot * G + h) * 128 + 16 * c + 2 * gq) = make_float2(x, y);
             } else {
               if (whole) {
-                const uint32_t w = pack_bf16x2(x * inv, y * inv);
+                const uint32_t w = pack_bf16x2(norm(x), norm(y));
                 p.out[head * 128 + 16 * c + gq] = static_cast<uint16_t>(w & 0xFFFFu);
                 p.out[head * 128 + 16 * c + 8 + gq] = static_cast<uint16_t>(w >> 16);
               } else {
@@ -710,11 +765,11 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
               }
             }
           }
-          if (gq == 0) store_stats(h, M, L);
+          if (gq == 0) store_stats(h, v);
         }
       }
     }
-    bar();  // scratch and (m, l) may be written again
+    bar();  // scratch and the warps' m, d, l may be written again
   };
 
   if (!kCluster || u1 > u0) load_query();
@@ -778,49 +833,81 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
         }
       }
       const bool in0 = rbase + gq < nvalid, in1 = rbase + 8 + gq < nvalid;
-      const float lv = kE4M3 ? meta.z : 0.f, iv = kE4M3 ? meta.w : kSumUnit;
+      const float lv = kE4M3 ? meta.z : 0.f;
       bool above = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float2 f = make_float2(p.scale_log2, p.scale_log2);
+        if constexpr (kE4M3) {
+          f = *reinterpret_cast<const float2*>(smem + T::OFF_QS + 4 * (8 * nt + 2 * t));
+          f.x *= meta.y, f.y *= meta.y;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float f = kE4M3 ? qf[nt][e & 1] * meta.y : qf[nt][e & 1];
-          const float s = (kChains == 2 ? sc[nt][e] + sd[kChains == 2 ? nt : 0][e] : sc[nt][e]) * f + lv;
+          const float s =
+              (kChains == 2 ? sc[nt][e] + sd[kChains == 2 ? nt : 0][e] : sc[nt][e]) * (e & 1 ? f.y : f.x) + lv;
           sc[nt][e] = ((e & 2) ? in1 : in0) ? s : -INFINITY;
-          above |= sc[nt][e] > m[nt][e & 1] + (kLift + 8.f);
         }
-      // m is the exponents' maximum less kLift, and only has to stay within 2^8
-      // of that: it moves when some row passes it by more, seldom after the
-      // first stages. P then reaches 2^15 at most, and f16 holds P down to
-      // 2^-32 of the greatest.
+        const float2 d = get_d(nt);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = kLift + kSlack;
+          if constexpr (kE4M3) top = fminf(top, kSlack + lv - (e ? d.y : d.x));
+          top += m[nt][e];
+          above |= sc[nt][e] > top || sc[nt][e + 2] > top;
+        }
+      }
+      // m is the exponents' maximum less kLift, m - d that of the scores, and both
+      // only have to stay within 2^kSlack of that: they move when some row passes
+      // one by more, seldom after the first stages. P then reaches 2^15 at most, and
+      // f16 holds P down to 2^-32 of the greatest.
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float2 d = get_d(nt);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            mx = fmaxf(mx - kLift, m[nt][e]);
-            const float alpha = mx == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mx);
-            m[nt][e] = mx;
-            l[nt][e] *= alpha;
+            const float was = m[nt][e], now = fmaxf(mx - kLift, was), alpha = rebase(was, now);
+            m[nt][e] = now;
+            if constexpr (kE4M3) {
+              const float old = e ? d.y : d.x, next = now - fmaxf(was - old, mx - lv);
+              l[nt][e] *= ex2_approx((was - now) + (next - old));
+              (e ? d.y : d.x) = next;
+            } else {
+              l[nt][e] *= alpha;
+            }
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               o[nt][c][e] *= alpha;
               o[nt][c][2 + e] *= alpha;
             }
           }
+          if constexpr (kE4M3) set_d(nt, d);
+        }
       }
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float pr[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(sc[nt][e] - m[nt][e & 1]);
-        l[nt][0] += (pr[0] + pr[2]) * iv;
-        l[nt][1] += (pr[1] + pr[3]) * iv;
+        for (int e = 0; e < 4; ++e) {
+          sc[nt][e] -= m[nt][e & 1];
+          pr[e] = ex2_approx(sc[nt][e]);
+        }
+        const float2 d = get_d(nt);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (kE4M3) {
+            const float by = (e ? d.y : d.x) - lv;
+            l[nt][e] += ex2_approx(sc[nt][e] + by) + ex2_approx(sc[nt][e + 2] + by);
+          } else {
+            l[nt][e] += pr[e] + pr[e + 2];
+          }
+        }
         pb[nt][0] = movmatrix_trans(kE4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
         pb[nt][1] = movmatrix_trans(kE4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
       }
@@ -890,16 +977,18 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     const int n = min(static_cast<int>(csize), cur.nst);
     for (int h = static_cast<int>(rank) * NCW + warp; h < G; h += static_cast<int>(csize) * NCW) {
       const uint32_t row = sums + static_cast<uint32_t>(h * kRow * 4);
-      float2 ml = make_float2(-INFINITY, 0.f);
+      float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
       if (lane < n) {
         const uint32_t at = peer_addr(row + 128 * 4, lane);
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(ml.x), "=f"(ml.y), "=f"(ml.z), "=f"(ml.w)
+                     : "r"(at)
+                     : "memory");
       }
-      float M = ml.x;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-      const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - M);  // no row: zeros, or a NaN
-      float L = 0.f;
+      float4 v = make_float4(warp_max(ml.x), 0.f, 0.f, 0.f);
+      const float unit = unit_of(ml, v.x), top = warp_max(unit), w = rebase(ml.x, v.x);
+      v.y = -top;
+      ml.z *= rebase(unit, top);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int r = 0; r < n; ++r) {
@@ -910,15 +999,14 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
                      : "r"(at)
                      : "memory");
         const float f = __shfl_sync(0xffffffffu, w, r);
-        L += f * __shfl_sync(0xffffffffu, ml.y, r);
+        v.z += __shfl_sync(0xffffffffu, ml.z, r);
         x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
       }
-      const float inv = L == 0.f ? 0.f : kSumUnit / L;
+      const Norm norm(v);
       const int64_t head = static_cast<int64_t>(cur.b) * p.Hq + cur.g * G + h;
       *reinterpret_cast<uint2*>(p.out + head * 128 + 4 * lane) =
-          make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-      if (p.lse && lane == 0)
-        p.lse[head] = L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
+          make_uint2(pack_bf16x2(norm(x.x), norm(x.y)), pack_bf16x2(norm(x.z), norm(x.w)));
+      if (p.lse && lane == 0) p.lse[head] = lse_of(v);
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
@@ -935,40 +1023,45 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
 // 4 us, 16 us as 4096 blocks of the first layout.
 constexpr int JOIN_WARPS = 8;
 
-// One head's partial rows mine, mine + step .. c1 of c0 .. c1: their sum of
-// weights and rows relative to the greatest maximum M of all. The first rows
-// are on their way while M is found.
+// One head's partial rows mine, mine + step .. c1 of c0 .. c1: their sum relative
+// to the greatest m of all, and v = (that m, d and l in the greatest unit of all).
+// The first rows are on their way while these are found.
 template <typename Slot>
-__device__ __forceinline__ void join_rows(const Params& p, Slot slot, int c0, int c1, int mine, int step, float& M,
-                                          float& L, float4& acc) {
+__device__ __forceinline__ void join_rows(const Params& p, Slot slot, int c0, int c1, int mine, int step, float4& v,
+                                          float4& acc) {
   const int lane = threadIdx.x & 31;
-  float2 ml[4];
-  float4 v[4];
+  float4 ml[4], y[4];
   auto fetch = [&](int c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ml[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c + i * step <= c1) {
         const int64_t s = slot(c + i * step);
         ml[i] = p.part_ml[s];
-        v[i] = reinterpret_cast<const float4*>(p.part_o + s * 128)[lane];
+        y[i] = reinterpret_cast<const float4*>(p.part_o + s * 128)[lane];
       }
     }
   };
   fetch(mine);
-  M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[slot(c)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  L = 0.f;
+  // this lane's greatest m and, relative to it, greatest unit
+  float4 a = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float4 x = p.part_ml[slot(c)];
+    const float M = fmaxf(a.x, x.x);
+    a.y = -fmaxf(unit_of(a, M), unit_of(x, M));
+    a.x = M;
+  }
+  v = make_float4(warp_max(a.x), 0.f, 0.f, 0.f);
+  const float top = warp_max(unit_of(a, v.x));
+  v.y = -top;
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = mine;;) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float w = ml[i].x == -INFINITY ? 1.f : ex2_approx(ml[i].x - M);  // no row: zeros, or a NaN
-      L += w * ml[i].y;
-      acc.x += w * v[i].x, acc.y += w * v[i].y, acc.z += w * v[i].z, acc.w += w * v[i].w;
+      const float w = rebase(ml[i].x, v.x);
+      v.z += ml[i].z * rebase(unit_of(ml[i], v.x), top);
+      acc.x += w * y[i].x, acc.y += w * y[i].y, acc.z += w * y[i].z, acc.w += w * y[i].w;
     }
     c += 4 * step;
     if (c > c1) break;
@@ -987,14 +1080,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
     const int c0 = end.z, c1 = blockIdx.x;
     for (int h = warp; h < p.G; h += JOIN_WARPS) {
       auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
-      float M, L;
-      float4 a;
-      join_rows(p, slot, c0, c1, c0, 1, M, L, a);
+      float4 v, a;
+      join_rows(p, slot, c0, c1, c0, 1, v, a);
       const int64_t head = static_cast<int64_t>(end.x) * p.Hq + end.y * p.G + h;
-      const float inv = L == 0.f ? 0.f : kSumUnit / L;
+      const Norm norm(v);
       *reinterpret_cast<uint2*>(p.out + head * 128 + 4 * lane) =
-          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-      if (p.lse && lane == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
+          make_uint2(pack_bf16x2(norm(a.x), norm(a.y)), pack_bf16x2(norm(a.z), norm(a.w)));
+      if (p.lse && lane == 0) p.lse[head] = lse_of(v);
     }
   } else {
     const int head = blockIdx.x, b = head / p.Hq, hq = head - b * p.Hq;
@@ -1008,22 +1100,21 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
     const int c0 = cut.run_of(first + g * cost + PAIR_COST), c1 = cut.run_of(first + (g + 1) * cost - 1);
     if (c0 == c1) return;
     auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
-    float M, L;
-    float4 acc;
-    join_rows(p, slot, c0, c1, c0 + warp, JOIN_WARPS, M, L, acc);
+    float4 v, acc;
+    join_rows(p, slot, c0, c1, c0 + warp, JOIN_WARPS, v, acc);
     s_o[warp][lane] = acc;
-    if (lane == 0) s_l[warp] = L;
+    if (lane == 0) s_l[warp] = v.z;
     __syncthreads();
     if (threadIdx.x >= 128) return;
     const float* so = reinterpret_cast<const float*>(s_o);
     const int64_t at = static_cast<int64_t>(head) * 128 + threadIdx.x;
     float x = 0.f;
-    L = 0.f;
+    v.z = 0.f;
 #pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w) x += so[128 * w + threadIdx.x], L += s_l[w];
-    const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : x * (kSumUnit / L));
+    for (int w = 0; w < JOIN_WARPS; ++w) x += so[128 * w + threadIdx.x], v.z += s_l[w];
+    const __nv_bfloat16 y = __float2bfloat16_rn(Norm(v)(x));
     p.out[at] = *reinterpret_cast<const uint16_t*>(&y);
-    if (p.lse && threadIdx.x == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + (log2f(L) + kSumUnitLog2)) * 0.6931471805599453f;
+    if (p.lse && threadIdx.x == 0) p.lse[head] = lse_of(v);
   }
 }
 

@@ -1070,7 +1070,7 @@ int kv_append_paged(const AppendArgs& a, cudaStream_t stream) {
 }
 
 // Workspace of decode_runs_kernel: units before each sequence, the pair that
-// ends in each run, then (m, l) and O of at most two partial results per run,
+// ends in each run, then (m, d, l) and O of at most two partial results per run,
 // each part 256-byte aligned.
 struct RunsWs {
   size_t ends_off, ml_off, o_off, total;
@@ -1079,7 +1079,7 @@ RunsWs runs_ws_layout(int64_t B, int64_t G) {
   RunsWs L;
   L.ends_off = align256(static_cast<size_t>(B + 1) * sizeof(int));
   L.ml_off = L.ends_off + align256(static_cast<size_t>(la::dpg::MAX_CTAS) * sizeof(int4));
-  L.o_off = L.ml_off + align256(static_cast<size_t>(2 * la::dpg::MAX_CTAS * G) * sizeof(float2));
+  L.o_off = L.ml_off + align256(static_cast<size_t>(2 * la::dpg::MAX_CTAS * G) * sizeof(float4));
   L.total = L.o_off + align256(static_cast<size_t>(2 * la::dpg::MAX_CTAS * G) * 128 * sizeof(float));
   return L;
 }
@@ -1151,7 +1151,7 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   p.lse = a.lse;
   p.prefix = reinterpret_cast<int*>(ws);
   p.ends = reinterpret_cast<int4*>(ws + L.ends_off);
-  p.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
+  p.part_ml = reinterpret_cast<float4*>(ws + L.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);
   p.epoch = next_epoch();
   const int resident = n_sm * (G > 8 ? la::dpg::Tile<kE4M3, true>::CTAS : la::dpg::Tile<kE4M3, false>::CTAS);

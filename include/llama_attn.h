@@ -458,8 +458,11 @@ size_t llama_attn_decode_runs_workspace_size(int B, int Hq, int Hkv, int D);
  *   out must not overlap q. Rows at or past cache_lens[b] are never used; a
  *   sequence of length 0 gives out = 0.
  * Codes of K and V are used exactly, scores, softmax sums and outputs are
- * float32; q and the softmax weights are rounded to 11 bits. The result does
- * not depend on timing. Errors and the other arguments as for
+ * float32, however far the scales of a sequence lie apart. q is rounded to 11
+ * bits (below 2^-14 of the row's greatest value to 2^-25 of that), and so is
+ * the product of a softmax weight and its value scale where values are summed
+ * (below 2^-21 of the head's greatest to 2^-32 of that). The result does not
+ * depend on timing. Errors and the other arguments as for
  * llama_attn_decode_paged.
  */
 int llama_attn_decode_paged_e4m3(const llama_attn_bf16 *q, const uint8_t *kpages, const uint8_t *vpages,

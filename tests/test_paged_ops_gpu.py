@@ -852,3 +852,97 @@ def test_sparse_decodes_need_their_block_ids():
         d = on_gpu(attention_state(kind, 64, 4, 1, [100], 57))
         with pytest.raises(ValueError, match="block_ids: tensor expected"):
             fn(d["q"], *d["pools"], *d["scales"], d["table"], None, d["lens"])
+
+
+def mixed_reference(s, lens, block_ids=None):
+    """out, lse, and the bounds of their errors, per head. The f16 weights are off by 2^-25 at most where the
+    greatest product of a weight and its value scale is at least 2^7: 2^-32 of the greatest, for each row, times a
+    code of at most 448. An exponent carries the logarithm of the value scale too (up to 119 in magnitude)."""
+    B, Hq, _ = s["q"].shape
+    Hkv, page = s["kp"].shape[1], s["page"]
+    G = Hq // Hkv
+    out, tol = torch.zeros(B, Hq, D, dtype=torch.float64), torch.zeros(B, Hq, D, dtype=torch.float64)
+    lse, lse_tol = torch.zeros(B, Hq, dtype=torch.float64), torch.zeros(B, Hq, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        q = R.rotate(s["q"][b], n, THETA)
+        for g in range(Hkv):
+            row = torch.arange(n)
+            if block_ids is not None:
+                row = torch.tensor([r for i in block_ids[b, g].tolist() if i >= 0
+                                    for r in range(i * page, min(n, (i + 1) * page))])
+            pg = s["table"][b, row // page].long()
+            k, v, vs = s["kv"][pg, g, row % page], s["vv"][pg, g, row % page], s["scales"][1][pg, g].double()
+            hs = slice(g * G, (g + 1) * G)
+            sc = q[hs] @ k.T / math.sqrt(D)
+            span = (q[hs].abs() @ k.abs().T / math.sqrt(D)).amax(-1)
+            p = torch.softmax(sc, -1)
+            out[b, hs], lse[b, hs] = p @ v, torch.logsumexp(sc, -1)
+            delta = 2.0 ** -11 * span + 2.0 ** -19 * (1 + sc.abs().amax(-1))
+            expo = delta + 2.0 ** -19 * vs.log2().abs().max()
+            tol[b, hs] = U["bf16"] * out[b, hs].abs() + (p @ v.abs()) * (torch.expm1(2 * expo) + 2.0 ** -10)[:, None] \
+                + len(row) * 2.0 ** -32 * 448 * (p * vs).amax(-1, keepdim=True) + 2.0 ** -133
+            lse_tol[b, hs] = delta + 2.0 ** -22 * (1 + sc.abs().amax(-1))
+    return out, lse, tol, lse_tol
+
+
+# value scales (exponents of two) of a sequence's blocks in turn, zeros in the blocks of the least of them
+MIXED = [[-100, 40], [40, -100], [-100, -100, 119], [119, -100, -100], [0, -100, 40, -60, 90], [-100, 30, 30, 30],
+         [-20, 0, 20]]
+
+
+@pytest.mark.parametrize("exps", MIXED)
+@pytest.mark.parametrize("Hq,Hkv,lens,slack", [
+    (4, 1, [128, 74, 640], 1),       # a cluster per pair; a stage of 10 rows in one warp alone
+    (24, 2, [128, 74, 640], 1),      # two tiles of heads
+    (8, 1, [3000, 128, 74], 1),      # blocks of both kinds in every CTA of a cluster, and CTAs of one kind
+    (2, 1, [20000, 700], 1),         # runs, joined by head
+    (16, 8, [20000, 128, 700], 1),   # runs, joined by run
+    (4, 1, [128, 74], 3000),         # runs for short sequences under a wide table
+])
+def test_decode_e4m3_value_scales_far_apart(exps, Hq, Hkv, lens, slack):
+    """A block counts in the denominator whatever its value scale is next to the others'."""
+    s = attention_state("e4m3", 64, Hq, Hkv, lens, 131)
+    s["table"] = torch.cat([s["table"], torch.full((len(lens), slack), -1, dtype=torch.int32)], 1)
+    for b, n in enumerate(lens):
+        for j in range(-(-n // 64)):
+            e = exps[j % len(exps)]
+            pg = int(s["table"][b, j])
+            s["scales"][1][pg] = 2.0 ** e
+            if e == -100:
+                s["vp"][pg, :, :max(0, min(64, n - 64 * j))] = 0
+    s["vv"] = R.codes(s["vp"]) * s["scales"][1].double()[:, :, None, None]
+    d = on_gpu(s)
+    lse = torch.empty(len(lens), Hq, device="cuda")
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], lse=lse)
+    o, l, tol, lse_tol = mixed_reference(s, lens)
+    assert torch.all((lse.double().cpu() - l).abs() <= lse_tol)
+    assert torch.all((out.double().cpu() - o).abs() <= tol)
+    ids = torch.full((len(lens), Hkv, 6), -1, dtype=torch.int32)
+    for b, n in enumerate(lens):  # a few blocks of both kinds
+        some = sorted({j * (-(-n // 64) - 1) // 5 for j in range(6)})
+        ids[b, :, :len(some)] = torch.tensor(some)
+    out = la.llama_attn_decode_paged_sparse_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], ids.cuda(), d["lens"],
+                                                 lse=lse)
+    o, l, tol, lse_tol = mixed_reference(s, lens, ids)
+    assert torch.all((lse.double().cpu() - l).abs() <= lse_tol)
+    assert torch.all((out.double().cpu() - o).abs() <= tol)
+
+
+@pytest.mark.parametrize("order", [0, 1])
+def test_decode_e4m3_greatest_score_and_greatest_value_scale_in_different_blocks(order):
+    """One block has the scores (they pass the others' by more than 2^130), the other the values: the softmax is the
+    first one's, and the second's values still count by what is left of their weights."""
+    lens = [128]
+    s = attention_state("e4m3", 64, 4, 2, lens, 137)
+    big, scored = (int(x) for x in (s["table"][0, :2] if order else s["table"][0, :2].flip(0)))
+    s["scales"][1][big], s["scales"][1][scored] = 2.0 ** 119, 2.0 ** -100
+    s["scales"][0][big], s["scales"][0][scored] = 2.0 ** -20, 2.0
+    s["kv"] = R.codes(s["kp"]) * s["scales"][0].double()[:, :, None, None]
+    s["vv"] = R.codes(s["vp"]) * s["scales"][1].double()[:, :, None, None]
+    d = on_gpu(s)
+    lse = torch.empty(1, 4, device="cuda")
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], lse=lse)
+    o, l, tol, lse_tol = mixed_reference(s, lens)
+    assert l.min() > 100  # far above the other block's scores, which are near 0
+    assert torch.all((lse.double().cpu() - l).abs() <= lse_tol)
+    assert torch.all((out.double().cpu() - o).abs() <= tol)
