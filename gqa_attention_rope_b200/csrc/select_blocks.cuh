@@ -16,7 +16,9 @@
 // Most blocks are far from the border, so the scores are first formed in
 // float32: a weight's rounding, 8 products and sums per lane and 5 sums over
 // the lanes stay within eps = 2^-20 sum_d |w_d| max |bound| (14 roundings of
-// 2^-24). A radix selection over these scores finds a range [lo, hi] that holds
+// 2^-24) and, where numbers are below float32's normal range, what that adds: 2^-150
+// for each of 256 weights, times max |bound|, and for each of fewer than 2^9 sums;
+// together below 2^-141 (max |bound| + 1). A radix selection over these scores finds a range [lo, hi] that holds
 // the one at the border; blocks outside [lo - 2 eps, hi + 2 eps] are decided by
 // it, and the few inside get their float64 score and are ranked by it.
 // For 64 sequences of 1024 to 32768 rows (8 KV heads, 64-row blocks, 71 MB of
@@ -329,12 +331,13 @@ __global__ void __launch_bounds__(NTHREADS, 4) select_blocks_kernel(const Params
     uint32_t mag = lane < static_cast<int>(csize) * NWARPS ? s_mag[lane] : 0u;
     if (lane + 32 < static_cast<int>(csize) * NWARPS) mag = max(mag, s_mag[lane + 32]);
     mag = __reduce_max_sync(0xffffffffu, mag);
-    const float eps2 = 2.f * 0x1p-20f * static_cast<float>(s_wsum[0] + s_wsum[1]) * __uint_as_float(mag);
+    const double bound = __uint_as_float(mag);
+    const float eps2 = __double2float_ru(2.0 * (0x1p-20 * (s_wsum[0] + s_wsum[1]) * bound + 0x1p-141 * (bound + 1.0)));
     uint32_t klo, khi;
     int unused;
     radix_select<false>(s_radix, approx, c0, c1, need, klo, khi, unused);
-    lo = score_of(klo) - eps2;
-    hi = score_of(khi) + eps2;
+    lo = __fsub_rd(score_of(klo), eps2);
+    hi = __fadd_ru(score_of(khi), eps2);
   }
   // 2: chosen, 1: near, 0: not chosen. A NaN is near, whatever else it is.
   auto decide = [&](int j) {

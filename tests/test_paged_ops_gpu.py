@@ -946,3 +946,20 @@ def test_decode_e4m3_greatest_score_and_greatest_value_scale_in_different_blocks
     assert l.min() > 100  # far above the other block's scores, which are near 0
     assert torch.all((lse.double().cpu() - l).abs() <= lse_tol)
     assert torch.all((out.double().cpu() - o).abs() <= tol)
+
+
+@pytest.mark.parametrize("q_scale,bound_scale", [(1e-25, 1e-19), (1e-22, 1e-22), (1e-38, 1.0), (1e-40, 1e30), (1.0, 3e-40),
+                                                 (1e30, 1e-38), (1e-20, 1e-28)])
+def test_select_below_the_normal_range_of_float32(q_scale, bound_scale):
+    """Scores, weights or bounds that float32 holds with few bits or none: the order is still float64's."""
+    Hq, Hkv, page, nb, B, n_sel = 8, 2, 64, 400, 6, 60
+    g = gen(15)
+    q = (torch.randn(B, Hq, D, generator=g) * q_scale).to(torch.bfloat16)
+    bounds = torch.randn(1, Hkv, 2, D, generator=g).sort(dim=2).values * torch.ones(nb * B, 1, 1, 1)
+    bounds[:, :, :, :8] *= 1 + torch.rand(nb * B, Hkv, 2, 8, generator=g) * 2.0 ** -6  # scores near one another
+    bounds = (bounds * bound_scale).to(torch.bfloat16)
+    table = torch.randperm(nb * B, generator=g).to(torch.int32).view(B, nb)
+    lens = [nb * page - b for b in range(B)]
+    ids = la.llama_attn_select_blocks(q.cuda(), bounds.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                      page, n_sel)
+    assert torch.equal(ids.cpu(), R.select(q, bounds, table, lens, page, n_sel, 1, 1, THETA))
