@@ -461,9 +461,10 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
           }
         }
         // the scales are needed only now, with the copies on their way; a value
-        // scale outside [2^-100, 2^119] would leave the exponent's range
+        // scale outside [2^-100, 2^119] would leave the exponent's range (a NaN stays)
         const float ks = __shfl_sync(0xffffffffu, now.ks, j);
-        const float vs = fminf(fmaxf(__shfl_sync(0xffffffffu, now.vs, j), 7.888609e-31f), 6.646140e35f);
+        float vs = __shfl_sync(0xffffffffu, now.vs, j);
+        vs = vs < 0x1p-100f ? 0x1p-100f : vs > 0x1p119f ? 0x1p119f : vs;
         if (lane == 0 && ok) {
           *reinterpret_cast<float4*>(smem + T::OFF_META + st * 16) =
               make_float4(__int_as_float(nvalid), ks, kE4M3 ? __log2f(vs) : 0.f, 0.f);

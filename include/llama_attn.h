@@ -448,7 +448,8 @@ size_t llama_attn_decode_runs_workspace_size(int B, int Hq, int Hkv, int D);
  * llama_attn_decode_paged against E4M3 pages:
  * out = softmax(q . (k_code k_scale) / sqrt(D)) (v_code v_scale), the scales
  * those of each row's page and KV head (any positive normal floats; those
- * outside [2^-100, 2^119] for values are taken as the nearest of the two).
+ * outside [2^-100, 2^119] for values are taken as the nearest of the two; a NaN
+ * makes its heads' outputs NaN).
  *
  *   lse           [B, Hq] float32 or NULL: log sum_j exp(score_j), as for
  *                 llama_attn_prefill_ex; -inf for a sequence without rows

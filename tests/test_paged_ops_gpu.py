@@ -963,3 +963,17 @@ def test_select_below_the_normal_range_of_float32(q_scale, bound_scale):
     ids = la.llama_attn_select_blocks(q.cuda(), bounds.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
                                       page, n_sel)
     assert torch.equal(ids.cpu(), R.select(q, bounds, table, lens, page, n_sel, 1, 1, THETA))
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("Hq,lens", [(4, [200, 64]), (20, [200, 64]), (4, [20000, 300])])
+def test_a_scale_that_is_nan_shows_in_its_heads(which, Hq, lens):
+    """A page whose scale was never written must not read as zeros: NaN in the heads that use it, nothing elsewhere."""
+    s = attention_state("e4m3", 64, Hq, 2, lens, 61)
+    d = on_gpu(s)
+    want = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"])
+    d["scales"][which][int(s["table"][0, (lens[0] - 1) // 64]), 1] = math.nan  # the last page of sequence 0, KV head 1
+    lse = torch.empty(2, Hq, device="cuda")
+    out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], lse=lse)
+    assert torch.isnan(out[0, Hq // 2:]).all() and torch.isnan(lse[0, Hq // 2:]).all()
+    assert torch.equal(out[0, :Hq // 2], want[0, :Hq // 2]) and torch.equal(out[1], want[1])
