@@ -13,6 +13,7 @@ LIB = os.path.join(PKG, "libllama_attn.so")
 INCLUDE = os.path.join(ROOT, "include")
 BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(PKG, "_binding.torch")
 
 
 def sources():
@@ -43,16 +44,36 @@ def _stale(target: str, files) -> bool:
     return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in files)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if force or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "llama_attn.h")]):
+def _torch_version() -> str:
+    import torch
+    return torch.__version__
+
+
+def build_binding(force: bool = False) -> str:
+    """The Python module. It holds torch's C++ interface, so another torch makes it stale too
+    (its stamp names the version that it was built against)."""
+    version = _torch_version()
+    built_for = None
+    if os.path.exists(BINDING_STAMP):
+        with open(BINDING_STAMP) as f:
+            built_for = f.read()
+    if force or built_for != version or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "llama_attn.h")]):
         tmp = BINDING + f".tmp{os.getpid()}"
         subprocess.check_call(binding_command(tmp))
         os.replace(tmp, BINDING)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(version)
+    return BINDING
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    # The library first: it needs nvcc only, and a C program needs nothing else.
     if force or _stale(LIB, sources()):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = nvcc_command(tmp, ["-Xptxas", "-v"] if verbose else [])
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 
