@@ -57,6 +57,7 @@
 
 #include "ptx.cuh"
 #include "rope.cuh"
+#include "runs.cuh"
 
 namespace la {
 namespace dpg {
@@ -65,7 +66,6 @@ constexpr int ROWS = 64;                  // cache rows of a stage
 constexpr int NRW = 4;                    // row groups: 16 rows of a stage each
 constexpr float kLift = 7.f;              // P of the greatest row: 2^7
 constexpr float kSlack = 8.f;             // the bounds move when a row passes them by more: P <= 2^15, weights <= 2^8
-constexpr int PAIR_COST = 6;              // a pair's begin and end, in units
 constexpr int MAX_CLUSTER = 16;
 constexpr int MAX_CTAS = 512;             // runs (and twice as many partial results) the workspace holds
 
@@ -138,36 +138,10 @@ __device__ __forceinline__ int stages_of(const Params& p, int b) {
   return ceil_div(len, ROWS);
 }
 
-// Cost of a pair of that many stages: what its begin and end take, then a unit per stage.
-__device__ __forceinline__ int cost_of(int nst) { return nst > 0 ? nst + PAIR_COST : 0; }
-
-// Position of a unit in the order (sequence, KV head, stage).
-struct Cursor {
-  int b, g, s, nst;
-};
-
 template <bool kSparse>
 __device__ __forceinline__ void advance(const Params& p, Cursor& c, int by) {
-  c.s += by;
-  while (c.b < p.B && c.s >= c.nst) {
-    c.s -= c.nst;
-    if (c.nst > 0 && ++c.g < p.Hkv) continue;
-    c.g = 0;
-    if (++c.b < p.B) c.nst = stages_of<kSparse>(p, c.b);
-  }
+  advance([&](int b) { return stages_of<kSparse>(p, b); }, p.B, p.Hkv, c, by);
 }
-
-// The cut of `total` units into n <= total runs: the first total % n of them
-// have one unit more than the others.
-struct Cut {
-  int q, r;
-  __device__ __forceinline__ Cut(int total, int n) : q(total / n), r(total - total / n * n) {}
-  __device__ __forceinline__ int start(int run) const { return q * run + min(run, r); }
-  __device__ __forceinline__ int run_of(int u) const {
-    const int big = r * (q + 1);
-    return u < big ? u / (q + 1) : r + (u - big) / q;
-  }
-};
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -335,16 +309,15 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
       int at = before.x, u = before.y;
       const int end = at + s_part[threadIdx.x].x;
       for (int b = my0; b < my1 && at <= c1 && c0 < end; ++b) {
-        const int nst = stages_of<kSparse>(p, b), cost = cost_of(nst), n = cost * p.Hkv;
+        const int nst = stages_of<kSparse>(p, b), n = cost_of(nst) * p.Hkv;
         if (at <= c0 && c0 < at + n) {
-          const int g = (c0 - at) / cost, off = c0 - at - g * cost;
-          s_start = make_int4(b, g, max(0, off - PAIR_COST), nst);
-          s_range.x = u + g * nst + max(0, off - PAIR_COST);
-          s_range.z = c0 - off + PAIR_COST;
+          const RunBegin begin(c0, at, u, nst);
+          s_start = make_int4(b, begin.g, begin.s, nst);
+          s_range.x = begin.unit;
+          s_range.z = begin.first_cost;
         }
         if (c1 < at + n) {
-          const int g = (c1 - at) / cost, off = c1 - at - g * cost;
-          s_range.y = u + g * nst + max(0, off + 1 - PAIR_COST);
+          s_range.y = run_end(c1, at, u, nst);
           break;
         }
         at += n, u += nst * p.Hkv;
@@ -625,7 +598,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
     }
     bar();
     const bool whole = first_unit >= u0 && last_unit <= u1;  // the segment lies inside this run
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_unit >= u0 ? 1 : 0);
+    const int64_t slot = slot_of(blockIdx.x, first_unit >= u0);
     if (!kCluster && first_unit < u0 && last_unit <= u1 && threadIdx.x == 0)
       p.ends[blockIdx.x] = make_int4(cur.b, cur.g, cut.run_of(first_cost), 0);
     // A head's m, and its (m, d, l), over the four warps.
@@ -1080,7 +1053,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
     if (end.x < 0) return;
     const int c0 = end.z, c1 = blockIdx.x;
     for (int h = warp; h < p.G; h += JOIN_WARPS) {
-      auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
+      auto slot = [&](int c) { return static_cast<int64_t>(slot_of(c, c == c0)) * p.G + h; };
       float4 v, a;
       join_rows(p, slot, c0, c1, c0, 1, v, a);
       const int64_t head = static_cast<int64_t>(end.x) * p.Hq + end.y * p.G + h;
@@ -1097,10 +1070,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
     const int total = p.prefix[p.B], first = p.prefix[b], end = p.prefix[b + 1];
     if (end == first) return;
     const Cut cut(total, min(max_runs, total));
-    const int cost = (end - first) / p.Hkv;
-    const int c0 = cut.run_of(first + g * cost + PAIR_COST), c1 = cut.run_of(first + (g + 1) * cost - 1);
+    const int cost = (end - first) / p.Hkv, at = first + g * cost;
+    const int c0 = first_run(cut, at), c1 = last_run(cut, at, cost - PAIR_COST);
     if (c0 == c1) return;
-    auto slot = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * p.G + h; };
+    auto slot = [&](int c) { return static_cast<int64_t>(slot_of(c, c == c0)) * p.G + h; };
     float4 v, acc;
     join_rows(p, slot, c0, c1, c0 + warp, JOIN_WARPS, v, acc);
     s_o[warp][lane] = acc;
@@ -1108,13 +1081,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) decode_join_kernel(const Para
     __syncthreads();
     if (threadIdx.x >= 128) return;
     const float* so = reinterpret_cast<const float*>(s_o);
-    const int64_t at = static_cast<int64_t>(head) * 128 + threadIdx.x;
+    const int64_t to = static_cast<int64_t>(head) * 128 + threadIdx.x;
     float x = 0.f;
     v.z = 0.f;
 #pragma unroll
     for (int w = 0; w < JOIN_WARPS; ++w) x += so[128 * w + threadIdx.x], v.z += s_l[w];
     const __nv_bfloat16 y = __float2bfloat16_rn(Norm(v)(x));
-    p.out[at] = *reinterpret_cast<const uint16_t*>(&y);
+    p.out[to] = *reinterpret_cast<const uint16_t*>(&y);
     if (p.lse && threadIdx.x == 0) p.lse[head] = lse_of(v);
   }
 }
