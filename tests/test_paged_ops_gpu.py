@@ -22,6 +22,7 @@ The 2^-19 (1 + |s|) covers float32 sums of 128 products (their errors are far
 below the worst case) and the exponent's and exponential's own rounding.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -977,3 +978,46 @@ def test_a_scale_that_is_nan_shows_in_its_heads(which, Hq, lens):
     out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"], lse=lse)
     assert torch.isnan(out[0, Hq // 2:]).all() and torch.isnan(lse[0, Hq // 2:]).all()
     assert torch.equal(out[0, :Hq // 2], want[0, :Hq // 2]) and torch.equal(out[1], want[1])
+
+
+def test_rope_bases_in_turn_and_from_two_threads():
+    """The frequencies follow the base of the call, whatever the call before had, on each host thread."""
+    page, Hq, Hkv, lens = 64, 8, 2, [700, 130]
+    s = attention_state("e4m3", page, Hq, Hkv, lens, 67)
+    d = on_gpu(s)
+    bounds = bounds_of(s)
+    bases = [10000.0, 500000.0, 1000000.0]
+    want_ids = [R.select(s["q"], bounds, s["table"], lens, page, 5, 1, 1, base) for base in bases]
+    want = [R.decode(s["q"], s["kv"], s["vv"], s["table"], lens, page, base) for base in bases]
+    kb = bounds.cuda()
+
+    def turn(order, results):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for i in order:
+                ids = la.llama_attn_select_blocks(d["q"], kb, d["table"], d["lens"], page, 5, rope_theta=bases[i])
+                out = la.llama_attn_decode_paged_e4m3(d["q"], *d["pools"], *d["scales"], d["table"], d["lens"],
+                                                      rope_theta=bases[i])
+                results.append((i, ids, out))
+        stream.synchronize()
+    torch.cuda.synchronize()
+    results = [], []
+    threads = [threading.Thread(target=turn, args=([0, 1, 2, 1, 0, 2] * 3, results[0])),
+               threading.Thread(target=turn, args=([2, 0, 0, 1, 2, 1] * 3, results[1]))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert [len(r) for r in results] == [18, 18]
+    for i, ids, out in results[0] + results[1]:
+        assert torch.equal(ids.cpu(), want_ids[i])
+        check_attention("e4m3", out, None, want[i], 7.0, 700)
+    # the append takes its angles from the caller's table
+    for base in bases:
+        st = append_state("bf16", page, Hkv, 5, [60, 0], None, 68)
+        rope = la.llama_attn_rope_table_build(st["table"].shape[1] * page, D, base)
+        got = run_append("bf16", st, [60, 0], rope, st["k"].cuda(), st["v"].cuda(), None)
+        ref = [p.double().clone() for p in st["pools"]]
+        R.append(st["k"], st["v"], ref, None, None, st["table"], [60, 0], st["new"], page, base)
+        # one bf16 rounding and 4 u32 (|x0| + |x1|), of values below 3 * 6
+        assert torch.all((got["pools"][0].cpu().double() - ref[0]).abs() <= U["bf16"] * ref[0].abs() + 4 * U["f32"] * 36)
