@@ -30,8 +30,10 @@
 // E4M3 codes become f16 exactly (cvt.rn.f16x2.e4m3x2), so K and V carry no
 // rounding beyond their own; Q is rounded to f16 after its row is brought to
 // [0.5, 1) by a power of two (2^-11 relative; bf16 would be 2^-8), P to f16.
-// On bf16 pages the products are bf16: Q is the sum of two bf16 terms (2^-16
-// relative), P one bf16 (2^-8, the rounding of the output's own type).
+// On bf16 pages the products are bf16: Q and P are sums of two bf16 terms (2^-16
+// relative). With one term for P (2^-8) the error to float64 was 2.3e-3 of the
+// outputs' size instead of the 1.7e-3 of the output's own rounding (16 sequences of
+// 8192-32768 rows, 64 blocks); the second term costs under 1% of the time.
 // The 8-bit rows are loaded with the 16-bit ldmatrix: each 32-bit register
 // then holds 4 neighbouring codes of a key, or 2 codes of 2 neighbouring rows
 // of V (transposed form). The products sum over d in any order, so Q is laid
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
                        const Params p) {
   using T = Tile<kE4M3, kWide>;
   constexpr int NT = T::NT, NCW = T::NCW, NTHREADS = T::NTHREADS;
-  constexpr int NQ = kE4M3 ? 1 : 2;  // terms of Q
+  constexpr int NQ = kE4M3 ? 1 : 2, NP = NQ;  // terms of Q and of P
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
@@ -863,7 +865,7 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
           if constexpr (kE4M3) set_d(nt, d);
         }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[NT][NP][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float pr[4];
@@ -882,8 +884,17 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
             l[nt][e] += pr[e] + pr[e + 2];
           }
         }
-        pb[nt][0] = movmatrix_trans(kE4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
-        pb[nt][1] = movmatrix_trans(kE4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (kE4M3) {
+            pb[nt][0][i] = movmatrix_trans(pack_f16x2(pr[2 * i], pr[2 * i + 1]));
+          } else {
+            const uint32_t hi = pack_bf16x2(pr[2 * i], pr[2 * i + 1]);
+            const float2 v = unpack_bf16x2(hi);
+            pb[nt][0][i] = movmatrix_trans(hi);
+            pb[nt][NP - 1][i] = movmatrix_trans(pack_bf16x2(pr[2 * i] - v.x, pr[2 * i + 1] - v.y));
+          }
+        }
       }
       // value rows at or past len may hold anything (NaN included): zero them so
       // that P = 0 cannot meet NaN inside the product.
@@ -910,8 +921,8 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
           const uint32_t b[4] = {f16x2_of_lo(w[2]), f16x2_of_hi(w[2]), f16x2_of_lo(w[3]), f16x2_of_hi(w[3])};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(o[nt][c], a, pb[nt][0], pb[nt][1]);
-            mma_f16_16816(o[nt][c + 1], b, pb[nt][0], pb[nt][1]);
+            mma_f16_16816(o[nt][c], a, pb[nt][0][0], pb[nt][0][1]);
+            mma_f16_16816(o[nt][c + 1], b, pb[nt][0][0], pb[nt][0][1]);
           }
         }
       } else {
@@ -922,7 +933,9 @@ __global__ void __launch_bounds__((Tile<kE4M3, kWide>::NTHREADS), (Tile<kE4M3, k
           uint32_t a0, a1, a2, a3;
           ldmatrix_x4_trans(vbase + (d8 >> 3) * T::HALF + sw128_off(row, d8 & 7), a0, a1, a2, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[nt][c], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          for (int term = 0; term < NP; ++term)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[nt][c], a0, a1, a2, a3, pb[nt][term][0], pb[nt][term][1]);
         }
       }
       if (tail) fence_proxy_async_smem();

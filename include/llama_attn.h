@@ -508,8 +508,8 @@ int llama_attn_select_blocks(const llama_attn_bf16 *q, const llama_attn_bf16 *kb
  * number of blocks are not read. An entry that breaks this sets
  * LLAMA_ATTN_DEVERR_BLOCK_IDS and contributes nothing; the output is then
  * unspecified. No id: out = 0, lse = -inf. Other arguments and errors as for
- * llama_attn_decode_paged_e4m3. On bf16 pages the softmax weights are rounded
- * to bf16 and q to 16 bits.
+ * llama_attn_decode_paged_e4m3. On bf16 pages q and the softmax weights are
+ * rounded to 16 bits.
  */
 int llama_attn_decode_paged_sparse(const llama_attn_bf16 *q, const llama_attn_bf16 *kpages,
                                    const llama_attn_bf16 *vpages, const int32_t *block_table,

@@ -1021,3 +1021,21 @@ def test_rope_bases_in_turn_and_from_two_threads():
         R.append(st["k"], st["v"], ref, None, None, st["table"], [60, 0], st["new"], page, base)
         # one bf16 rounding and 4 u32 (|x0| + |x1|), of values below 3 * 6
         assert torch.all((got["pools"][0].cpu().double() - ref[0]).abs() <= U["bf16"] * ref[0].abs() + 4 * U["f32"] * 36)
+
+
+@pytest.mark.parametrize("Hq,Hkv,lens,n_sel", [(8, 2, [1000, 64, 3000], 7), (24, 2, [1000, 64, 3000], 7),
+                                               (16, 8, [777, 2049, 640] * 16, 7)])
+def test_sparse_bf16_weights_carry_16_bits(Hq, Hkv, lens, n_sel):
+    """Over bf16 pages a softmax weight is the sum of two bf16 terms (2^-16), as the query is: beyond the output's own
+    rounding the error is far below that of one term (2^-8)."""
+    s = attention_state("bf16", 64, Hq, Hkv, lens, 141)
+    d = on_gpu(s)
+    bounds = bounds_of(s)
+    ids = la.llama_attn_select_blocks(d["q"], bounds.cuda(), d["table"], d["lens"], 64, n_sel)
+    out = la.llama_attn_decode_paged_sparse(d["q"], *d["pools"], d["table"], ids, d["lens"])
+    o, lse, mass, span = R.decode(s["q"], s["kv"], s["vv"], s["table"], lens, 64, THETA, 0, ids.cpu())
+    delta = 2.0 ** -16 * span + 2.0 ** -19 * (1 + lse.abs() + span)
+    # 2^-16 of the weights; 2^-16 more for float32 sums of up to 448 rows in 16-row products (28 roundings of 2^-24)
+    # and the exponential's own 2^-22
+    tol = U["bf16"] * o.abs() + mass * (torch.expm1(2 * delta) + 2.0 ** -15)[..., None]
+    assert torch.all((out.double().cpu() - o).abs() <= tol)
