@@ -20,10 +20,12 @@
 // apart took more (registers of the rare path spill: 59 to 64 us).
 //
 // What bounds it: HBM. A row of an E4M3 cache is 256 bytes for 4 * 128 * G
-// flop. 64 sequences of 1024 to 32768 rows, 64 heads over 8: 341 us, 6490 GB/s
-// (99% of a copy's rate); two tiles of heads (G > 8) 4600 GB/s, bound by a
-// warp's chain of conversions, products and exponentials; short caches by latency
-// (one sequence of 1000 rows, 32 heads: 5.5 us).
+// flop. Times here are of a call in a CUDA graph of ten; a program's calls one after
+// another take 0.5 us (short ones) to 3% more. 64 sequences of 1024 to 32768 rows,
+// 64 heads over 8: 342 us, 6480 GB/s (99% of a copy's rate; 350 us and 97% as calls);
+// two tiles of heads (G > 8) 58 us for 131072 rows, 4630 GB/s, bound by a warp's
+// chain of conversions, products and exponentials (168 registers, 60 to 88 bytes
+// spilled); short caches by latency (one sequence of 1000 rows, 32 heads: 5.6 us).
 // The products run on mma.sync m16n8k16 with the 16 cache rows of a warp as M
 // and the heads of the group as N (8 or 16): S^T = K Q^T, O^T = V^T P^T.
 // With heads as M, groups of 8 heads would leave half of each product empty.
@@ -52,7 +54,9 @@
 // the order of the runs: the result does not depend on timing.
 // Short batches have a second form: a cluster of CTAs per (sequence, head), which
 // cut its stages among themselves and join their results through one another's
-// shared memory; no kernel follows (one sequence of 1000 rows 5.5 us, 7.8 as runs).
+// shared memory; no kernel follows (one sequence of 1000 rows 5.6 us, 8.0 as runs).
+// The block table's width decides, since the host does not know the lengths: under
+// a table of many blocks short sequences run in the first form.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -79,7 +83,8 @@ struct Tile {
   static constexpr int NCW = NRW;
   static constexpr int NTHREADS = (NCW + 1) * 32;
   // Both tiles in one warp, 2 CTAs per SM, query in registers: one 131072-row
-  // sequence under 128 heads 58.5 us; 3 CTAs with the query in shared memory
+  // sequence under 128 heads 58.5 us (all of these with one exponential for both
+  // sums, in its first form); 3 CTAs with the query in shared memory
   // (128 registers) 76 us; a tile per warp and eight compute warps (every code
   // converted twice) 63 us; the next stage's scores formed before this one's
   // values (spills) 80 us. One tile for 64 heads over 8: 341 us for the 70B

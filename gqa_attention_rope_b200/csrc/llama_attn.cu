@@ -1058,6 +1058,8 @@ int kv_append_paged(const AppendArgs& a, cudaStream_t stream) {
   // sequences: 4.8 us with 128 x 2, 7.6 with 128 x 8, 11.7 with 256 x 8. A 131072-
   // token prompt into E4M3 pages of 64 rows: 184 us with 128 x 8, 324 with 256 x
   // 8; of 128 rows: 260 with 128 x 8 (a page is read twice), 193 with 256 x 8.
+  // Pages of more rows are read and turned twice: of 192 rows 316 us, of 256 265,
+  // of 512 271.
   const int rows = a.T < a.page_size ? a.T : a.page_size;
   auto launch = [&](void (*kernel)(la::pap::Params), int threads, int rows_per_thread) {
     return launch_dependent(kernel, grid, threads, kE4M3 ? threads * rows_per_thread * 32 : 0, stream, 1, p);
@@ -1162,14 +1164,14 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   // A cluster per pair where the pairs fit on the device at once and are short:
   // no second kernel, no run with more than one pair. Its size is the largest of
   // which all are resident, above 8 from 32 stages on. Clusters and runs, 8 KV
-  // heads: one sequence of 1000 rows 5.5 and 7.8 us (16 CTAs per pair: 6.2), of
-  // 4000 7.8 and 9.0 (8 CTAs: 8.4), of 12000 12.0 and 11.5; 10 of 2000 (3 CTAs)
-  // 11.5 and 12.6; 32 of 250 (1 CTA) 6.7 and 11.0. Lengths of a batch may be far
+  // heads: one sequence of 1000 rows 5.5 and 8.0 us (16 CTAs per pair: 6.1), of
+  // 4000 7.8 and 9.4 (8 CTAs: 8.4), of 12000 12.2 and 11.7; 10 of 2000 (3 CTAs)
+  // 11.4 and 12.7; 32 of 250 (1 CTA) 6.8 and 11.3. Lengths of a batch may be far
   // below the table's: the longest then waits for its own CTAs alone. From 16
-  // stages per CTA on that costs as much as is won (8 of 4000 rows 16.3 and 18.8
-  // us, of 1 to 4000 13.2 and 11.7; of 1 to 2000 9.0 and 9.7). Chosen blocks
-  // are mostly as many for each sequence: 16 of 64 blocks of 64 rows, 64 heads,
-  // 64.0 and 68.0 us with the choice.
+  // stages per CTA on that costs as much as is won (8 of 4000 rows 16.5 and 19.2
+  // us, of 1 to 4000 13.3 and 12.1; of 1 to 2000 9.1 and 10.0). Chosen blocks
+  // are mostly as many for each sequence: 16 of 64 blocks of 64 rows, E4M3, 64
+  // heads, 46.2 and 52.1 us with the choice.
   const int64_t pairs = static_cast<int64_t>(a.B) * a.Hkv;
   const int64_t stages = static_cast<int64_t>(kSparse && a.n_sel < a.max_blocks ? a.n_sel : a.max_blocks) *
                          (a.page_size / la::dpg::ROWS);  // of a pair at most
@@ -1198,9 +1200,9 @@ int decode_runs(const RunsArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return LLAMA_ATTN_ERR_CUDA;
   // A pair spans grid / (B * Hkv) runs on average; from 8 on its partial rows
   // are enough for the eight warps of a block. Join by run and by head: 64
-  // sequences of 8 KV heads, sparse, 124 and 134 us in all; 8 of 32000 rows 88
-  // and 88; one of 32000 rows 22.6 and 20.1; one of 131072 under 128 heads 64
-  // and 55.
+  // sequences of 8 KV heads, sparse, 124 and 135 us in all; 8 of 32000 rows 89
+  // and 90; one of 32000 rows 24.2 and 20.5; one of 131072 under 128 heads 70
+  // and 58.
   const bool by_run = static_cast<int64_t>(a.B) * a.Hkv * 8 > grid;
   return cuda_status(launch_dependent(by_run ? la::dpg::decode_join_kernel<true> : la::dpg::decode_join_kernel<false>,
                                       dim3(by_run ? grid : a.B * a.Hq), la::dpg::JOIN_WARPS * 32, 0, stream, 1, p,
@@ -1313,8 +1315,8 @@ int llama_attn_select_blocks(const llama_attn_bf16* q, const llama_attn_bf16* kb
   p.freqs = rope_freqs(rope_theta);
   // Clusters widen while every CTA stays resident (four per SM) and has at
   // least one pass (8 warps x 8 blocks) of its own. Selection and sparse decode
-  // of one sequence of 2048 blocks (8 KV heads) with 1, 2, 4, 8 CTAs: 52, 37, 30,
-  // 27 us; of 16 sequences 82, 75, 71, 78; of 64 136, 139, 147, 169.
+  // of one sequence of 2048 blocks (8 KV heads) with 1, 2, 4, 8 CTAs: 47, 34, 27,
+  // 24 us; of 16 sequences 55, 49, 44, 48; of 64 126, 131, 137, 156.
   const int64_t groups = static_cast<int64_t>(B) * Hkv;
   int csize = 1;
   while (csize < 8 && groups * csize * 2 <= 4 * n_sm && max_blocks > csize * la::sel::NWARPS * 8) csize *= 2;

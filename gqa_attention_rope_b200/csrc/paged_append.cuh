@@ -18,17 +18,21 @@
 //
 // Work split: one CTA owns K or V of one (sequence, logical block, KV head),
 // so the block's amax, scale and bounds need no atomics. 16 threads take a row,
-// 16 bytes each, and a thread up to 8 rows. The bound is the memory traffic
-// (512 bytes read and 256 (E4M3) or 512 (bf16) written per token and head) and,
-// for E4M3 keys, issue and latency: all loads of a thread are issued before
+// 16 bytes each, and a thread up to 8 rows. All loads of a thread are issued before
 // the first is used, and before the page is looked up (rows past the end read
-// the last row again instead of branching). Measured: four 8192-token prompts
-// of 8 KV heads into bf16 pages 49 us (5840 GB/s of the bytes it cannot do
-// without), a 131072-token prompt into E4M3 pages 193 us (4540 GB/s; K and V in
-// one CTA of 512 threads took 704 us). Of that prompt the keys alone take 140
-// us and the values 78: the keys' rotation, ranges, scale and coding are about
-// 12 instructions per element. A persistent form that loads the next head's
-// rows while one is coded was 4% faster on 64-row pages and slower on others.
+// the last row again instead of branching). bf16 pages are bound by the memory
+// traffic (512 bytes read and 512 written per token and head): four 8192-token
+// prompts of 8 KV heads 49 us in a CUDA graph, 50 as calls (5730 GB/s of the bytes
+// it cannot do without, 87% of a copy's rate).
+// E4M3 pages (256 bytes written) are bound by waiting: a 131072-token prompt into
+// 128-row pages takes 193 us in a graph, 200 as calls (4380 GB/s; K and V in one CTA
+// of 512 threads took 704 us), with 49% of the DRAM rate, 45% of the issue slots
+// and 36% of the warps. The keys alone take 140 us and the values 78: a key row is
+// copied to shared memory, read, turned, written back as float32 until its block's
+// scale is known, and read again, and 64 KB for that leave three CTAs on an SM.
+// Pages of 64 rows 184 us, of 256 265 (every key fetched and turned twice). A
+// persistent form that loads the next head's rows while one is coded was 4%
+// faster on 64-row pages and slower on others.
 #pragma once
 
 #include "ptx.cuh"

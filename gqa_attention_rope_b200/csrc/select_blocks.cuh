@@ -22,7 +22,7 @@
 // the one at the border; blocks outside [lo - 2 eps, hi + 2 eps] are decided by
 // it, and the few inside get their float64 score and are ranked by it.
 // For 64 sequences of 1024 to 32768 rows (8 KV heads, 64-row blocks, 71 MB of
-// bounds) that takes 30 us; all scores in float64 39 us; scores on the tensor
+// bounds) that takes 28 us; all scores in float64 39 us; scores on the tensor
 // cores (three bf16 terms of the weights as columns of one product) 42 us, with
 // a bound of 2^-15 only, which left several blocks near.
 //

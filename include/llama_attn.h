@@ -373,7 +373,11 @@ int llama_attn_decode_noalloc(const llama_attn_bf16 *q, const llama_attn_bf16 *k
  * The calls below share llama_attn_decode_paged's cache (page pool, block
  * table, lengths) and its limits: D == 128, page_size a multiple of 64, B and
  * Hkv at most 65535, max_blocks * page_size and n_pages * Hkv * page_size below
- * 2^31 rows (else LLAMA_ATTN_ERR_UNSUPPORTED). A "block" is one page's worth
+ * 2^31 rows (else LLAMA_ATTN_ERR_UNSUPPORTED, as where a call's own counts
+ * pass its limits: an append of rows to more than 65535 pages of a sequence, a
+ * row_stride above 2^31 or a batch_stride above 2^47, a decode with
+ * B * Hkv * (max_blocks * page_size / 64 + 6) above 2^31, a selection with Hq
+ * above 65535). A "block" is one page's worth
  * of consecutive rows of one sequence; block j of sequence b is page
  * block_table[b * max_blocks + j]. Tensors are 16-byte aligned. None of the
  * calls allocates or synchronises; each may be captured into a CUDA graph. Two
@@ -418,6 +422,10 @@ int llama_attn_decode_noalloc(const llama_attn_bf16 *q, const llama_attn_bf16 *k
  * v_scales of a block whose first row is appended need no initialisation.
  * NaN and infinite inputs give unspecified codes, scales and bounds in their
  * own block.
+ * llama_attn_decode_paged rotates its query at cache_lens[b], the position
+ * behind the cache, and has no q_pos_offset: where the token's own key has been
+ * appended to bf16 pages, llama_attn_decode_paged_sparse with every block chosen
+ * and q_pos_offset = -1 is the decode over all rows.
  * A length or a new length out of range sets LLAMA_ATTN_DEVERR_CACHE_LEN and
  * that sequence is left as it was (out_lens[b] = cache_lens[b]); a page id
  * outside [0, n_pages) sets LLAMA_ATTN_DEVERR_BLOCK_TABLE and that block's
@@ -477,8 +485,8 @@ int llama_attn_decode_paged_e4m3(const llama_attn_bf16 *q, const uint8_t *kpages
  * Chooses the blocks that a decode should read, per sequence and KV head:
  * block j scores sum over the query heads h of the KV group of
  * sum_d max(q_hd lo_jd, q_hd hi_jd), an upper bound of the summed products of
- * the rotated queries with any key of the block (lo, hi: its kbounds),
- * computed in float64.
+ * the rotated queries with any key of the block as bf16 pages hold it (lo, hi:
+ * its kbounds; an E4M3 code may pass them by its rounding), computed in float64.
  *
  *   q          [B, Hq, D] un-rotated, rotated at cache_lens[b] + q_pos_offset
  *   kbounds    [n_pages, Hkv, 2, D] bf16, as llama_attn_kv_append_paged writes it
