@@ -192,7 +192,8 @@ __device__ __forceinline__ float unit_of(const float4& v, float M) { return v.x 
 // From O to the output, 2^d / l, for v = (m, d, l). d lies within [-115, 120] (value
 // scales within [2^-100, 2^119], m behind the greatest exponent by kLift to kLift +
 // kSlack, m - d behind the greatest score by up to kSlack) and l may be as great as
-// 2^39, so neither factor alone leaves float32's range.
+// 2^39 (on bf16 pages d is 0 and l at most 2^46), so neither factor alone leaves
+// float32's range.
 struct Norm {
   float inv, f;
   __device__ __forceinline__ explicit Norm(const float4& v) : inv(v.z == 0.f ? 0.f : 1.f / v.z), f(v.z == 0.f ? 0.f : ex2_approx(v.y)) {}

@@ -21,7 +21,7 @@
 #include "paged_append.cuh"
 #include "select_blocks.cuh"
 
-#define LLAMA_ATTN_VERSION 400  // 0.4.0: paged-cache append, E4M3 paged decode, block-sparse decode
+#define LLAMA_ATTN_VERSION 401  // 0.4.1: the paged decodes of 0.4.0 with a larger workspace
 
 namespace {
 

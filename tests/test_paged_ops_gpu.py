@@ -1039,3 +1039,61 @@ def test_sparse_bf16_weights_carry_16_bits(Hq, Hkv, lens, n_sel):
     # and the exponential's own 2^-22
     tol = U["bf16"] * o.abs() + mass * (torch.expm1(2 * delta) + 2.0 ** -15)[..., None]
     assert torch.all((out.double().cpu() - o).abs() <= tol)
+
+
+@pytest.mark.parametrize("Hq,Hkv,slack", [
+    (8, 2, 0),      # clusters
+    (24, 2, 0),     # clusters, two tiles of heads
+    (2, 1, 3000),   # runs, joined by head
+    (16, 8, 3000),  # runs, joined by run
+    (12, 1, 3000),  # runs, two tiles of heads
+])
+def test_captured_e4m3_decodes_replay_with_new_lengths_on_two_streams(Hq, Hkv, slack):
+    """Every form of the decode in a CUDA graph: two graphs with a workspace each, replayed at the same time, take
+    lengths, scales and chosen blocks as they are then."""
+    page, lens = 64, [900, 64, 300, 1]
+    s = attention_state("e4m3", page, Hq, Hkv, lens, 151)
+    for b, n in enumerate(lens):  # all rows valid: shorter lengths later leave live rows behind the end
+        for j in range(-(-n // page)):
+            s["kp"][int(s["table"][b, j])] &= 0x77
+            s["vp"][int(s["table"][b, j])] &= 0x77
+    s["table"] = torch.cat([s["table"], torch.full((4, slack), -1, dtype=torch.int32)], 1)
+    s["kv"] = R.codes(s["kp"]) * s["scales"][0].double()[:, :, None, None]
+    d = on_gpu(s)
+    sides = []
+    for i in range(2):
+        stream, lens_d = torch.cuda.Stream(), d["lens"].clone()
+        vs = (d["scales"][1] * (i + 1)).contiguous()
+        ids = torch.full((4, Hkv, 3), -1, dtype=torch.int32, device="cuda")
+        outs = [torch.empty_like(d["q"]) for _ in range(2)]
+        ws = torch.empty(la.llama_attn_decode_runs_workspace_size(4, Hq, Hkv), dtype=torch.uint8, device="cuda")
+        bounds = bounds_of(s).cuda()
+
+        def step(outs=outs, lens_d=lens_d, vs=vs, ids=ids, ws=ws, bounds=bounds):
+            pool = (*d["pools"], d["scales"][0], vs, d["table"])
+            la.llama_attn_decode_paged_e4m3(d["q"], *pool, lens_d, out=outs[0], workspace=ws)
+            la.llama_attn_select_blocks(d["q"], bounds, d["table"], lens_d, page, 3, block_ids=ids)
+            la.llama_attn_decode_paged_sparse_e4m3(d["q"], *pool, ids, lens_d, out=outs[1], workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+        sides.append((graph, stream, lens_d, vs, ids, outs, step))
+    for now in ([900, 64, 300, 1], [0, 1, 299, 0], [65, 0, 1, 1], [900, 63, 0, 1]):
+        for graph, stream, lens_d, *_ in sides:
+            lens_d.copy_(torch.tensor(now, dtype=torch.int32))
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for graph, stream, *_ in sides:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for i, (_, _, lens_d, vs, ids, outs, step) in enumerate(sides):
+            got = [x.clone() for x in outs] + [ids.clone()]
+            vv = R.codes(s["vp"]) * vs.cpu().double()[:, :, None, None]
+            for out, chosen in ((got[0], None), (got[1], got[2].cpu())):
+                ref = R.decode(s["q"], s["kv"], vv, s["table"], now, page, THETA, 0, chosen)
+                check_attention("e4m3", out, None, ref, 2 * 7.0, 900)
+            step()  # the same calls outside a graph: the same bits
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(got, outs + [ids]))
